@@ -70,7 +70,7 @@ def draw(rng):
         V = 256 * 131072 // T
     hist = rng.choice([0, _log(rng, 1, 16384 if T <= 32 else 2048)])
     return dict(op="logits", T=T, V=V, hist=hist, bias=rng.choice([0, _log(rng, 1, 300)]),
-                masks=rng.choice([0, rng.randint(1, 32)]), want=rng.choice(["out", "pick", "both"]), pad=rng.choice([0, 0, 1, 5, 8]))
+                masks=rng.choice([0, rng.randint(1, 32)]), want=rng.choice(["out", "both"] if T > 4 else ["out", "both", "pick"]), pad=rng.choice([0, 0, 1, 5, 8]))
 
 
 def work(case):
