@@ -76,6 +76,11 @@ enum {
                                               experts in [0, E), but its weights are undefined */
 #define MOE_Q4_STATUS_BAD_EXPERT_INDEX 0x8u /* the permutation met an expert index outside [0, E)
                                                (counted as expert 0; the top-k never produces one) */
+#define MOE_Q4_STATUS_BAD_ADAPTER_INDEX 0x10u /* an adapter index outside [-1, n_adapters) (its row is
+                                                 treated as one without an adapter) */
+#define MOE_Q4_STATUS_BAD_MASK_INDEX 0x20u /* a mask index outside [-1, n_masks) (nothing is allowed in
+                                              its row) */
+#define MOE_Q4_STATUS_NAN_LOGIT 0x40u      /* an allowed logit was NaN (see moe_q4_logits_apply) */
 
 /* One MoE layer.  Expert e's matrices are consecutive Q4_0 blocks:
  *   w_gate, w_up : [n_experts][ffn][hidden/32] blocks (18 B each)
@@ -251,6 +256,120 @@ int moe_q4_ffn_forward_streamed(const moe_q4_layer* L, const float* x, int64_t T
 size_t moe_q4_gemv_workspace_bytes(int64_t T, int32_t H);
 int moe_q4_gemv(const uint8_t* W, int64_t N, int32_t H, const float* x, int64_t T, float* y, void* workspace,
                 size_t ws_bytes, moe_q4_stream_t stream);
+
+/* ---------------------------------------------------------------------
+ * Low-rank adapters of many requests beside a shared projection.
+ *
+ * The 4-bit matrices stay frozen and shared by all requests; each request may
+ * bring a low-rank correction of its own.  With a = adapter[t],
+ *     y[t] = base[t] + scale[a] * B_a (A_a x[t])      (a >= 0)
+ *     y[t] = base[t]                                  (a == -1: no adapter)
+ * beside moe_q4_gemv (x its input, base its output, N the vocabulary) or
+ * beside the expert layer (x and base the input and output of
+ * moe_q4_ffn_forward, N = hidden).  The paper has no counterpart.
+ *   - x [T] rows of hidden fp32 at a pitch of ldx elements (ldx >= hidden, a
+ *     multiple of 4); base and y [T] rows of n_out fp32 at pitches ldb and
+ *     ldy (>= n_out, any).  base NULL: zeros.  base == y with ldb == ldy:
+ *     in place, rows without an adapter are then neither read nor written.
+ *   - adapter [T] int32 on the device, in any order; an index outside
+ *     [-1, n_adapters) counts as -1 and sets MOE_Q4_STATUS_BAD_ADAPTER_INDEX.
+ *   - a and b are fp32, binary16 or bfloat16 (dtype), never rounded; x and
+ *     A x keep 22 significant bits or more and all sums are fp32.  A lower
+ *     rank than `rank` is stored with zero rows of a / columns of b.
+ *   - A row's result depends on that row and its adapter, on T through the
+ *     choice of kernel, and on nothing else in the batch; the same call gives
+ *     the same bits.
+ *   - hidden a positive multiple of 256 up to 16384; rank a multiple of 8,
+ *     8 <= rank <= 128 (else MOE_Q4_ERR_SHAPE); 1 <= n_out <= 2^30;
+ *     1 <= n_adapters <= 1024.  x, a, b 16-byte aligned, the other arrays
+ *     4-byte, the workspace 256-byte.
+ *   - y may not overlap x, adapter, the adapters or the workspace, nor base
+ *     except in place; rows of x, base and y may interleave as column ranges
+ *     of one wider buffer (equal pitches).
+ *   - The workspace (moe_q4_adapters_workspace_bytes(A, T) bytes, its first
+ *     uint32 the status word, written by this call) may not be shared by
+ *     calls that overlap on the GPU.  No host synchronisation; capturable.
+ * --------------------------------------------------------------------- */
+enum { MOE_Q4_F32 = 0, MOE_Q4_F16 = 1, MOE_Q4_BF16 = 2 };
+
+typedef struct {
+    int32_t hidden;     /* H: columns of every A */
+    int32_t rank;       /* r */
+    int64_t n_out;      /* N: rows of every B */
+    int32_t n_adapters;
+    int32_t dtype;      /* MOE_Q4_F32, MOE_Q4_F16 or MOE_Q4_BF16: elements of a and b */
+    const void* a;      /* [n_adapters][rank][hidden] */
+    const void* b;      /* [n_adapters][n_out][rank] */
+    const float* scale; /* [n_adapters], or NULL: 1 */
+} moe_q4_adapters;
+
+/* Bytes of device workspace moe_q4_adapters_apply needs for up to T_max rows
+ * (0 on invalid arguments). */
+size_t moe_q4_adapters_workspace_bytes(const moe_q4_adapters* A, int64_t T_max);
+int moe_q4_adapters_apply(const moe_q4_adapters* A, const float* x, int64_t ldx, const int32_t* adapter, int64_t T,
+                          const float* base, int64_t ldb, float* y, int64_t ldy, void* workspace, size_t ws_bytes,
+                          moe_q4_stream_t stream);
+
+/* ---------------------------------------------------------------------
+ * Logit rules: penalties for repeated tokens, biases and grammar masks on
+ * the logits of moe_q4_gemv, and the greedy token of what is left.
+ *
+ * For row t and token v with logit l, s = v occurs in the row's history, c =
+ * how often it was generated there (every step is one binary32 rounding):
+ *     l = l > 0 ? l / repetition[t] : l * repetition[t]      where s
+ *     l = (l - frequency[t] * c) - presence[t]               where c > 0
+ *     l = l + bias                                            where the row lists v
+ *     l = -inf                                                where the mask lacks v
+ * The paper has no counterpart.
+ *   - History: row t's tokens are tokens[row_start[t] .. row_start[t+1]), those
+ *     at positions >= generated_start[t] were generated (generated_start
+ *     NULL: all of them), the ones before came with the prompt.  Tokens
+ *     outside [0, vocab) are skipped (padding).  row_start NULL: no history.
+ *     A row has fewer than 2^30 tokens.
+ *   - repetition (> 0), presence, frequency: [T] or NULL (1, 0, 0).
+ *   - Bias: row t lists bias_token / bias_value [bias_start[t] ..
+ *     bias_start[t+1]); of a token listed twice the later entry counts;
+ *     tokens outside [0, vocab) are skipped; -inf bans a token.  bias_start
+ *     NULL: none.
+ *   - Mask: n_masks rows of ceil(vocab/32) words, bit v%32 of word v/32 set
+ *     where v is allowed; row t uses mask mask_row[t], -1: everything is
+ *     allowed; mask_row NULL: mask t (n_masks == T).  A masked logit is -inf
+ *     whatever it was.  mask NULL: none.
+ *   - Start positions outside [0, n_tokens] or [0, n_bias] are clamped to it.
+ * Outputs, each optional but at least one:
+ *   out [T] rows of vocab fp32 at pitch ld_out: the processed logits
+ *     (out == logits with the same pitch: in place; no other overlap).
+ *   token [T] int32: the largest processed logit's token, the lowest one on
+ *     ties; -1 where no logit is above -inf.  NaN ranks below every number.
+ *   lse [T] fp32: log(sum_v exp(processed logit)), so that token's
+ *     log-probability is its logit less lse; -inf where nothing is left, NaN
+ *     where an allowed logit is NaN.
+ * status (device uint32, may be NULL): MOE_Q4_STATUS_BAD_MASK_INDEX and, when
+ * token or lse is asked for, MOE_Q4_STATUS_NAN_LOGIT are OR-ed into it.
+ * 1 <= vocab <= 2^30, pitches >= vocab; T <= 2^24; all arrays 4-byte
+ * aligned, the start arrays 8-byte, tokens 16-byte.  No workspace, no host
+ * synchronisation; capturable.
+ * --------------------------------------------------------------------- */
+typedef struct {
+    int64_t vocab;
+    const int32_t* tokens;          /* [n_tokens] */
+    int64_t n_tokens;
+    const int64_t* row_start;       /* [T+1] or NULL */
+    const int64_t* generated_start; /* [T] or NULL */
+    const float* repetition;        /* [T] or NULL */
+    const float* presence;          /* [T] or NULL */
+    const float* frequency;         /* [T] or NULL */
+    const int32_t* bias_token;      /* [n_bias] */
+    const float* bias_value;        /* [n_bias] */
+    int64_t n_bias;
+    const int64_t* bias_start;      /* [T+1] or NULL */
+    const uint32_t* mask;           /* [n_masks][ceil(vocab/32)] or NULL */
+    int64_t n_masks;
+    const int32_t* mask_row;        /* [T] or NULL */
+} moe_q4_logit_rules;
+
+int moe_q4_logits_apply(const moe_q4_logit_rules* R, const float* logits, int64_t ld, int64_t T, float* out,
+                        int64_t ld_out, int32_t* token, float* lse, uint32_t* status, moe_q4_stream_t stream);
 
 /* Static description of an error code. */
 const char* moe_q4_status_string(int status);

@@ -35,6 +35,9 @@ STATUS_SCALE_OVERFLOW = 0x1
 STATUS_SPIN_TIMEOUT = 0x2
 STATUS_NONFINITE_LOGIT = 0x4
 STATUS_BAD_EXPERT_INDEX = 0x8
+STATUS_BAD_ADAPTER_INDEX = 0x10
+STATUS_BAD_MASK_INDEX = 0x20
+STATUS_NAN_LOGIT = 0x40
 
 PATH_AUTO, PATH_GROUPED_DP4A, PATH_DECODE, PATH_TENSOR_CORE = 0, 1, 2, 3
 PATH_TENSOR_CORE_N32, PATH_TENSOR_CORE_N128, PATH_TENSOR_CORE_N64 = 4, 5, 6
@@ -49,7 +52,8 @@ EXPORTS = ["moe_q4_quantize_act", "moe_q4_route", "moe_q4_ffn_workspace_bytes", 
            "moe_q4_ffn_forward_noalloc", "moe_q4_last_cuda_error", "moe_q4_residual_rmsnorm",
            "moe_q4_stack_workspace_bytes", "moe_q4_stack_forward", "moe_q4_gemv_workspace_bytes", "moe_q4_gemv",
            "moe_q4_staging_bytes", "moe_q4_ffn_forward_streamed", "moe_q4_test_override_device",
-           "moe_q4_rescale_ceiling"]
+           "moe_q4_rescale_ceiling", "moe_q4_adapters_workspace_bytes", "moe_q4_adapters_apply",
+           "moe_q4_logits_apply"]
 
 
 class MoeQ4Error(RuntimeError):
@@ -77,6 +81,21 @@ class _Debug(ctypes.Structure):
                 ("block_dots_out", ctypes.c_void_p), ("block_dots_down", ctypes.c_int32),
                 ("block_dots_group", ctypes.c_int32), ("block_dots_rb", ctypes.c_int32),
                 ("decode_kernel_ns", ctypes.c_void_p)]
+
+
+class _Adapters(ctypes.Structure):
+    _fields_ = [("hidden", ctypes.c_int32), ("rank", ctypes.c_int32), ("n_out", ctypes.c_int64),
+                ("n_adapters", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
+
+
+class _LogitRules(ctypes.Structure):
+    _fields_ = [("vocab", ctypes.c_int64), ("tokens", ctypes.c_void_p), ("n_tokens", ctypes.c_int64),
+                ("row_start", ctypes.c_void_p), ("generated_start", ctypes.c_void_p),
+                ("repetition", ctypes.c_void_p), ("presence", ctypes.c_void_p), ("frequency", ctypes.c_void_p),
+                ("bias_token", ctypes.c_void_p), ("bias_value", ctypes.c_void_p), ("n_bias", ctypes.c_int64),
+                ("bias_start", ctypes.c_void_p), ("mask", ctypes.c_void_p), ("n_masks", ctypes.c_int64),
+                ("mask_row", ctypes.c_void_p)]
 
 
 def _load() -> ctypes.CDLL:
@@ -108,6 +127,9 @@ def _load() -> ctypes.CDLL:
         "moe_q4_ffn_forward_streamed": ([P, P, i64, P, P, sz, P, sz, P], ctypes.c_int),
         "moe_q4_test_override_device": ([i32, i32, i32], ctypes.c_int),
         "moe_q4_rescale_ceiling": ([i32, i32, P, P, P], ctypes.c_int),
+        "moe_q4_adapters_workspace_bytes": ([P, i64], sz),
+        "moe_q4_adapters_apply": ([P, P, i64, P, i64, P, i64, P, i64, P, sz, P], ctypes.c_int),
+        "moe_q4_logits_apply": ([P, P, i64, i64, P, i64, P, P, P, P], ctypes.c_int),
     }
     for name, (args, res) in sigs.items():
         f = getattr(lib, name)
@@ -370,6 +392,146 @@ def moe_q4_gemv(W: torch.Tensor, x: torch.Tensor, y=None, workspace=None, stream
     _check(_lib.moe_q4_gemv(_p(W), N, H, _p(x), T, _p(y), _p(workspace), workspace.numel(), _stream(stream)),
            "moe_q4_gemv")
     return y
+
+
+# ---------------------------------------------------------------- per-request operators around the projections
+
+def _rows(t: torch.Tensor, name: str, device, cols=None, rows=None) -> int:
+    """The row pitch of a 2D fp32 tensor on `device` with contiguous rows."""
+    if t.dtype != torch.float32 or t.dim() != 2 or t.device != device:
+        raise ValueError(f"{name} must be a 2D float32 tensor on {device}")
+    if (cols is not None and t.shape[1] != cols) or (rows is not None and t.shape[0] != rows):
+        raise ValueError(f"{name} is {tuple(t.shape)}, expected ({rows}, {cols})")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _vector(t, name: str, device, dtype, n=None):
+    """The address of a contiguous 1D tensor of n elements, or None."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.dim() != 1 or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous 1D {dtype} tensor on {device}")
+    if n is not None and t.shape[0] != n:
+        raise ValueError(f"{name} has {t.shape[0]} elements, expected {n}")
+    return t.data_ptr()
+
+
+class Adapters:
+    """Low-rank adapters on the device and their C descriptor.
+
+    a [n, r, H] and b [n, N, r] (both float32, float16 or bfloat16,
+    contiguous), scale [n] float32 or None (1).  Adapter i adds
+    scale[i] * b[i] (a[i] x) to a projection of x."""
+
+    _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+
+    def __init__(self, a: torch.Tensor, b: torch.Tensor, scale: Optional[torch.Tensor] = None):
+        if a.dim() != 3 or b.dim() != 3 or a.shape[0] != b.shape[0] or a.shape[1] != b.shape[2]:
+            raise ValueError("a must be [n, r, H] and b [n, N, r]")
+        if a.dtype not in self._DTYPES or a.dtype != b.dtype or a.device != b.device:
+            raise ValueError("a and b must be float32, float16 or bfloat16, alike, on one device")
+        if not a.is_cuda or not a.is_contiguous() or not b.is_contiguous():
+            raise ValueError("a and b must be contiguous, on a GPU")
+        self.a, self.b, self.scale, self.device = a, b, scale, a.device
+        self.n_adapters, self.rank, self.hidden = a.shape
+        self.n_out = b.shape[1]
+        self.struct = _Adapters(self.hidden, self.rank, self.n_out, self.n_adapters, self._DTYPES[a.dtype],
+                                a.data_ptr(), b.data_ptr(),
+                                _vector(scale, "scale", self.device, torch.float32, self.n_adapters))
+
+    @property
+    def ref(self):
+        return ctypes.byref(self.struct)
+
+
+def moe_q4_adapters_workspace_bytes(adapters: Adapters, T_max: int) -> int:
+    return int(_lib.moe_q4_adapters_workspace_bytes(adapters.ref, int(T_max)))
+
+
+def moe_q4_adapters_apply(adapters: Adapters, x: torch.Tensor, adapter: torch.Tensor, base=None, y=None,
+                          workspace=None, stream=None):
+    """y[t] = base[t] + scale[e] * b[e] (a[e] x[t]) with e = adapter[t] (int32;
+    -1: y[t] = base[t]).  base None: zeros; y may be base (in place).  x, base
+    and y may be column slices of wider buffers (contiguous rows)."""
+    dev = adapters.device
+    T = x.shape[0]
+    ldx = _rows(x, "x", dev, adapters.hidden)
+    ids = _vector(adapter, "adapter", dev, torch.int32, T)
+    y = torch.empty((T, adapters.n_out), dtype=torch.float32, device=dev) if y is None else y
+    ldy = _rows(y, "y", dev, adapters.n_out, T)
+    ldb = 0 if base is None else _rows(base, "base", dev, adapters.n_out, T)
+    if workspace is None:
+        workspace = alloc_workspace(moe_q4_adapters_workspace_bytes(adapters, T), dev)
+    with torch.cuda.device(dev):
+        _check(_lib.moe_q4_adapters_apply(adapters.ref, _p(x), ldx, ids, T, _p(base), ldb, _p(y), ldy, _p(workspace),
+                                          workspace.numel(), _stream(stream)), "moe_q4_adapters_apply")
+    return y
+
+
+class LogitRules:
+    """What each row of a batch of logits is ruled by (see moe_q4_logit_rules
+    in include/moe_q4.h); every part may be left out.
+
+    tokens int32 [n], row_start int64 [T+1], generated_start int64 [T]: the
+    rows' histories; repetition, presence, frequency float32 [T];
+    bias_token int32 [m], bias_value float32 [m], bias_start int64 [T+1];
+    mask int32 [n_masks, ceil(vocab/32)] (a bit per token, set: allowed),
+    mask_row int32 [T] (-1: no mask) or None (mask t for row t)."""
+
+    def __init__(self, tokens=None, row_start=None, generated_start=None, repetition=None, presence=None,
+                 frequency=None, bias_token=None, bias_value=None, bias_start=None, mask=None, mask_row=None):
+        if (tokens is None) != (row_start is None):
+            raise ValueError("tokens and row_start belong together")
+        if not (bias_token is None) == (bias_value is None) == (bias_start is None):
+            raise ValueError("bias_token, bias_value and bias_start belong together")
+        self.tensors = dict(tokens=tokens, row_start=row_start, generated_start=generated_start,
+                            repetition=repetition, presence=presence, frequency=frequency, bias_token=bias_token,
+                            bias_value=bias_value, bias_start=bias_start, mask=mask, mask_row=mask_row)
+
+    def struct(self, T: int, V: int, device) -> _LogitRules:
+        """The C descriptor for T rows of V logits."""
+        t = self.tensors
+        i32, i64, f32 = torch.int32, torch.int64, torch.float32
+
+        def ptr(name, dtype, n=None):
+            return _vector(t[name], name, device, dtype, n)
+        mask = t["mask"]
+        if mask is not None and (mask.dtype != i32 or mask.dim() != 2 or mask.shape[1] != (V + 31) // 32 or
+                                 mask.device != device or not mask.is_contiguous()):
+            raise ValueError(f"mask must be a contiguous [n_masks, {(V + 31) // 32}] int32 tensor on {device}")
+        n_bias = 0 if t["bias_token"] is None else t["bias_token"].shape[0]
+        return _LogitRules(
+            V, ptr("tokens", i32), 0 if t["tokens"] is None else t["tokens"].shape[0], ptr("row_start", i64, T + 1),
+            ptr("generated_start", i64, T), ptr("repetition", f32, T), ptr("presence", f32, T),
+            ptr("frequency", f32, T), ptr("bias_token", i32), ptr("bias_value", f32, n_bias), n_bias,
+            ptr("bias_start", i64, T + 1), None if mask is None else mask.data_ptr(),
+            0 if mask is None else mask.shape[0], ptr("mask_row", i32, T))
+
+
+def moe_q4_logits_apply(rules: LogitRules, logits: torch.Tensor, out=None, token=None, lse=None, status=None,
+                        stream=None):
+    """Rules the logits [T, V] (fp32).  Writes the outputs that are given: out
+    [T, V] fp32 (the processed logits; may be `logits`), token [T] int32 (the
+    greedy token, -1 where nothing is left), lse [T] fp32 (log-sum-exp); with
+    none given, a new out.  Returns (out, token, lse)."""
+    if not logits.is_cuda or logits.dim() != 2:
+        raise ValueError("logits must be a 2D tensor on a GPU")
+    T, V = logits.shape
+    dev = logits.device
+    ld = _rows(logits, "logits", dev)
+    if out is None and token is None and lse is None:
+        out = torch.empty((T, V), dtype=torch.float32, device=dev)
+    ldo = 0 if out is None else _rows(out, "out", dev, V, T)
+    r = rules.struct(T, V, dev)
+    with torch.cuda.device(dev):
+        _check(_lib.moe_q4_logits_apply(ctypes.byref(r), _p(logits), ld, T, _p(out), ldo,
+                                        _vector(token, "token", dev, torch.int32, T),
+                                        _vector(lse, "lse", dev, torch.float32, T),
+                                        _vector(status, "status", dev, torch.int32, 1), _stream(stream)),
+               "moe_q4_logits_apply")
+    return out, token, lse
 
 
 # ---------------------------------------------------------------- host-streamed experts

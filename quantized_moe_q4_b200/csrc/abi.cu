@@ -560,6 +560,134 @@ int moe_q4_gemv(const uint8_t* W, int64_t N, int32_t H, const float* x, int64_t 
     return cuda_rc(launch_gemv_dp4a(W, N, H, qa, da, (int)T, y, status, dev, s));
 }
 
+// Whether rows of `wa` floats at pitch lda from a and rows of `wb` floats at
+// pitch ldb from b share an element.  Ranges that overlap are still disjoint
+// where both are column ranges of one buffer: equal pitches, and the columns
+// of one clear of the other's in every row.
+static bool rows_overlap(const float* a, int64_t lda, int64_t wa, const float* b, int64_t ldb, int64_t wb, int64_t T) {
+    const size_t na = sizeof(float) * (size_t)((T - 1) * lda + wa), nb = sizeof(float) * (size_t)((T - 1) * ldb + wb);
+    if (!overlap(a, na, b, nb)) return false;
+    const intptr_t bytes = reinterpret_cast<intptr_t>(b) - reinterpret_cast<intptr_t>(a);
+    if (lda != ldb || bytes % (intptr_t)sizeof(float)) return true;
+    int64_t col = (int64_t)(bytes / (intptr_t)sizeof(float)) % lda;  // b's first column in a's rows
+    if (col < 0) col += lda;
+    return col < wa || col + wb > lda;
+}
+
+static int check_adapters(const moe_q4_adapters* A) {
+    if (!A || !A->a || !A->b) return MOE_Q4_ERR_INVALID_ARG;
+    if (A->n_out < 1 || A->n_out > (int64_t(1) << 30) || A->n_adapters < 1 || A->n_adapters > 1024 ||
+        (A->dtype != MOE_Q4_F32 && A->dtype != MOE_Q4_F16 && A->dtype != MOE_Q4_BF16))
+        return MOE_Q4_ERR_INVALID_ARG;
+    if (A->hidden <= 0 || A->hidden % 256 || A->hidden > 16384 || A->rank < 8 || A->rank > 128 || A->rank % 8)
+        return MOE_Q4_ERR_SHAPE;
+    if (!aligned(A->a, 16) || !aligned(A->b, 16) || !aligned(A->scale, 4)) return MOE_Q4_ERR_ALIGN;
+    return MOE_Q4_OK;
+}
+
+static constexpr int64_t PITCH_LIMIT = int64_t(1) << 32;
+
+size_t moe_q4_adapters_workspace_bytes(const moe_q4_adapters* A, int64_t T_max) {
+    if (check_adapters(A) || T_max < 0 || T_max > T_LIMIT) return 0;
+    return adapters_layout(A->n_adapters, std::max<int64_t>(T_max, 1), nullptr, nullptr);
+}
+
+int moe_q4_adapters_apply(const moe_q4_adapters* A, const float* x, int64_t ldx, const int32_t* adapter, int64_t T,
+                          const float* base, int64_t ldb, float* y, int64_t ldy, void* workspace, size_t ws_bytes,
+                          moe_q4_stream_t stream) {
+    int rc = check_adapters(A);
+    if (rc) return rc;
+    if (T < 0 || T > T_LIMIT) return MOE_Q4_ERR_INVALID_ARG;
+    if (T == 0) return MOE_Q4_OK;
+    if (!x || !adapter || !y || !workspace) return MOE_Q4_ERR_INVALID_ARG;
+    const int64_t H = A->hidden, N = A->n_out;
+    if (ldx < H || ldx > PITCH_LIMIT || ldy < N || ldy > PITCH_LIMIT || (base && (ldb < N || ldb > PITCH_LIMIT)))
+        return MOE_Q4_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || ldx % 4 || !aligned(adapter, 4) || !aligned(base, 4) || !aligned(y, 4) ||
+        !aligned(workspace, 256))
+        return MOE_Q4_ERR_ALIGN;
+    AdapterArgs p;
+    const size_t need = adapters_layout(A->n_adapters, T, static_cast<char*>(workspace), &p);
+    if (ws_bytes < need) return MOE_Q4_ERR_WORKSPACE;
+    const size_t ybytes = sizeof(float) * (size_t)((T - 1) * ldy + N), elt = A->dtype == MOE_Q4_F32 ? 4 : 2;
+    const size_t wbytes = elt * (size_t)A->n_adapters * (size_t)A->rank;
+    if (rows_overlap(x, ldx, H, y, ldy, N, T) || overlap(y, ybytes, adapter, sizeof(int32_t) * (size_t)T) ||
+        overlap(y, ybytes, workspace, need) || overlap(y, ybytes, A->a, wbytes * (size_t)H) ||
+        overlap(y, ybytes, A->b, wbytes * (size_t)N) ||
+        (A->scale && overlap(y, ybytes, A->scale, sizeof(float) * (size_t)A->n_adapters)) ||
+        (base && !(base == y && ldb == ldy) && rows_overlap(base, ldb, N, y, ldy, N, T)))
+        return MOE_Q4_ERR_OVERLAP;
+    DeviceInfo dev;
+    rc = current_device(&dev);
+    if (rc) return rc;
+    p.a = A->a; p.b = A->b; p.scale = A->scale;
+    p.x = x; p.ids = adapter; p.base = base; p.y = y;
+    p.ldx = ldx; p.ldb = ldb; p.ldy = ldy; p.N = N; p.T = T;
+    p.H = A->hidden; p.r = A->rank; p.n = A->n_adapters;
+    return cuda_rc(launch_adapters(p, A->dtype, dev, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int moe_q4_logits_apply(const moe_q4_logit_rules* R, const float* logits, int64_t ld, int64_t T, float* out,
+                        int64_t ld_out, int32_t* token, float* lse, uint32_t* status, moe_q4_stream_t stream) {
+    if (!R || R->vocab < 1 || R->vocab > (int64_t(1) << 30) || T < 0 || T > T_LIMIT) return MOE_Q4_ERR_INVALID_ARG;
+    const bool hist = R->row_start != nullptr, bias = R->bias_start != nullptr, mask = R->mask != nullptr;
+    if ((hist && (R->n_tokens < 0 || (R->n_tokens && !R->tokens))) ||
+        (bias && (R->n_bias < 0 || (R->n_bias && (!R->bias_token || !R->bias_value)))) ||
+        (mask && (R->n_masks < 1 || (!R->mask_row && R->n_masks != T))))
+        return MOE_Q4_ERR_INVALID_ARG;
+    if (T == 0) return MOE_Q4_OK;
+    if (!logits || (!out && !token && !lse)) return MOE_Q4_ERR_INVALID_ARG;
+    const int64_t V = R->vocab;
+    if (ld < V || ld > PITCH_LIMIT || (out && (ld_out < V || ld_out > PITCH_LIMIT))) return MOE_Q4_ERR_INVALID_ARG;
+    const void* p4[] = {logits, out, token, lse, status, R->repetition, R->presence, R->frequency, R->bias_token,
+                        R->bias_value, R->mask, R->mask_row};
+    for (const void* q : p4)
+        if (!aligned(q, 4)) return MOE_Q4_ERR_ALIGN;
+    if (!aligned(R->row_start, 8) || !aligned(R->generated_start, 8) || !aligned(R->bias_start, 8) ||
+        (hist && !aligned(R->tokens, 16)))
+        return MOE_Q4_ERR_ALIGN;
+    // every output against every input and against the other outputs
+    const size_t rows = (size_t)T, words = (size_t)((V + 31) / 32);
+    struct Span { const void* p; size_t n; };
+    const Span outs[] = {{out, out ? 4 * ((rows - 1) * (size_t)ld_out + (size_t)V) : 0},
+                         {token, token ? 4 * rows : 0},
+                         {lse, lse ? 4 * rows : 0},
+                         {status, status ? size_t(4) : 0}};
+    const Span ins[] = {{hist ? R->tokens : nullptr, hist ? 4 * (size_t)R->n_tokens : 0},
+                        {R->row_start, hist ? 8 * (rows + 1) : 0},
+                        {R->generated_start, hist && R->generated_start ? 8 * rows : 0},
+                        {R->repetition, R->repetition ? 4 * rows : 0},
+                        {R->presence, R->presence ? 4 * rows : 0},
+                        {R->frequency, R->frequency ? 4 * rows : 0},
+                        {R->bias_token, bias ? 4 * (size_t)R->n_bias : 0},
+                        {R->bias_value, bias ? 4 * (size_t)R->n_bias : 0},
+                        {R->bias_start, bias ? 8 * (rows + 1) : 0},
+                        {R->mask, mask ? 4 * words * (size_t)R->n_masks : 0},
+                        {R->mask_row, mask && R->mask_row ? 4 * rows : 0}};
+    for (int i = 0; i < 4; ++i) {
+        for (const Span& q : ins)
+            if (overlap(outs[i].p, outs[i].n, q.p, q.n)) return MOE_Q4_ERR_OVERLAP;
+        for (int j = 0; j < i; ++j)
+            if (overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return MOE_Q4_ERR_OVERLAP;
+        if (i && overlap(outs[i].p, outs[i].n, logits, 4 * ((rows - 1) * (size_t)ld + (size_t)V)))
+            return MOE_Q4_ERR_OVERLAP;
+    }
+    if (out && !(out == logits && ld_out == ld) && rows_overlap(logits, ld, V, out, ld_out, V, T))
+        return MOE_Q4_ERR_OVERLAP;
+    DeviceInfo dev;
+    int rc = current_device(&dev);
+    if (rc) return rc;
+    LogitArgs p;
+    p.logits = logits; p.out = out; p.token = token; p.lse = lse; p.status = status;
+    p.ld = ld; p.ldo = ld_out; p.V = V; p.T = T;
+    p.tokens = R->tokens; p.row_start = R->n_tokens ? R->row_start : nullptr; p.generated = R->generated_start;
+    p.rep = R->repetition; p.pres = R->presence; p.freq = R->frequency;
+    p.bias_token = R->bias_token; p.bias_value = R->bias_value; p.bias_start = R->n_bias ? R->bias_start : nullptr;
+    p.mask = R->mask; p.mask_row = R->mask_row;
+    p.n_tokens = R->n_tokens; p.n_bias = R->n_bias; p.n_masks = R->n_masks;
+    return cuda_rc(launch_logits(p, dev, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 // Staging copy of a layer's experts on the device: gate [E] | up [E] | down [E]
 // | shared gate | shared up | shared down, each region 256-byte aligned.
 static void staging_layout(const moe_q4_layer* L, size_t off[7]) {

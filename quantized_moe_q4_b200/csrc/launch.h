@@ -137,6 +137,52 @@ cudaError_t launch_stage_experts(const StageParams& p, const DeviceInfo& dev, cu
 cudaError_t launch_residual_rmsnorm(float* x, const float* y, int64_t T, int H, float eps, float* xn,
                                     cudaStream_t s);
 
+// k_adapters.cu: low-rank adapters of many requests.
+struct AdapterArgs {
+    const void* a;       // [n][r][H]
+    const void* b;       // [n][N][r]
+    const float* scale;  // [n] or NULL
+    const float* x;
+    const int32_t* ids;  // [T]
+    const float* base;   // may be NULL (zeros) or y (in place)
+    float* y;
+    int64_t ldx, ldb, ldy, N, T;
+    int H, r, n;
+    // workspace
+    uint32_t* status;
+    int32_t* n_tiles;
+    int32_t* perm;       // [T] rows grouped by adapter
+    int4* tiles;         // {adapter (-1: none), first position in perm, rows, 0}
+    int32_t* chunk_cnt;  // [chunks][n + 2]
+    int32_t* chunk_base; // [chunks][n + 1]
+};
+// Bytes of the workspace for T rows; with base, fills the workspace pointers.
+size_t adapters_layout(int n, int64_t T, char* base, AdapterArgs* p);
+cudaError_t launch_adapters(const AdapterArgs& p, int dtype, const DeviceInfo& dev, cudaStream_t s);
+
+// k_logits.cu: logit rules.
+struct LogitArgs {
+    const float* logits;
+    float* out;        // may be NULL or logits (in place)
+    int32_t* token;    // may be NULL
+    float* lse;        // may be NULL
+    uint32_t* status;  // may be NULL
+    int64_t ld, ldo, V, T;
+    const int32_t* tokens;
+    const int64_t* row_start;
+    const int64_t* generated;
+    const float* rep;
+    const float* pres;
+    const float* freq;
+    const int32_t* bias_token;
+    const float* bias_value;
+    const int64_t* bias_start;
+    const uint32_t* mask;
+    const int32_t* mask_row;
+    int64_t n_tokens, n_bias, n_masks;
+};
+cudaError_t launch_logits(const LogitArgs& p, const DeviceInfo& dev, cudaStream_t s);
+
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // MOE_Q4_OK if the current device is compute capability 10.0, else
