@@ -21,6 +21,7 @@
 #include "common.cuh"
 #include "launch.h"
 #include "ptx.cuh"
+#include "tc.cuh"
 
 namespace moeq4 {
 
@@ -35,6 +36,7 @@ constexpr int GROUP_THREADS = 1024;
 constexpr int GROUP_IDS = 16;     // ids per thread of the grouping kernels
 constexpr int GROUP_CHUNK = GROUP_THREADS * GROUP_IDS;
 constexpr int MAX_ADAPTERS = 1024;
+constexpr int TILE_MIN_ROWS = 16; // rows per adapter from which the tile kernel is used
 
 // ------------------------------------------------------------------ clusters
 
@@ -56,6 +58,19 @@ __device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
+__device__ __forceinline__ void st_cluster4(uint32_t addr, float4 v) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+                 : "memory");
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
 // ------------------------------------------------------------------ weights
 
 // Eight consecutive elements (16-byte aligned) as binary32, exactly.
@@ -64,8 +79,7 @@ __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
-__device__ __forceinline__ void load8(const __half* p, float (&v)[8]) {
-    const uint4 q = __ldg(reinterpret_cast<const uint4*>(p));
+__device__ __forceinline__ void unpack8(uint4 q, float (&v)[8], const __half*) {
     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -73,14 +87,17 @@ __device__ __forceinline__ void load8(const __half* p, float (&v)[8]) {
         v[2 * i + 1] = half_bits_to_float(w[i] >> 16);
     }
 }
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-    const uint4 q = __ldg(reinterpret_cast<const uint4*>(p));
+__device__ __forceinline__ void unpack8(uint4 q, float (&v)[8], const __nv_bfloat16*) {
     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         v[2 * i] = __uint_as_float(w[i] << 16);
         v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
+}
+template <class W>
+__device__ __forceinline__ void load8(const W* p, float (&v)[8]) {
+    unpack8(__ldg(reinterpret_cast<const uint4*>(p)), v, p);
 }
 
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
@@ -300,6 +317,341 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(THREADS)
         expand_columns<W, 8>(b, p, s_tok, cnt, s_u, n0, n1);
 }
 
+// ------------------------------------------------------------------ tile kernel
+//
+// Many rows: tiles of 128 rows of one adapter on the tensor cores, tf32 with
+// binary32 accumulators.  A binary32 value is split into two tf32 parts of 11
+// significant bits, v = hi + lo up to 2^-22 |v|; binary16 and bfloat16 weights
+// are tf32 values already, so a product with them takes two MMAs, and one of
+// two binary32 values three (lo * lo, 2^-22 of the product, is left out).
+//   1. u' = x A^T: each CTA of the cluster sums over its eighth of H.
+//      M = the tile's rows, N = r, operands K-major in 32-column panels with
+//      128-byte rows swizzled in 16-byte units (SWIZZLE_128B).
+//   2. the eight partial sums are joined through distributed shared memory:
+//      CTA c adds rows 16 c .. 16 c + 15 in rank order and hands them to all.
+//   3. d^T = B u^T over the CTA's blocks of 128 columns of y: M = columns of y,
+//      N = the tile's rows, so that a TMEM lane is a column and every access
+//      of base and y is 32 consecutive floats, whatever their alignment.
+// TMEM is held inside steps 1 and 3 only, never across a cluster barrier: a
+// CTA that holds some waits for nothing but its own MMAs, so CTAs that wait
+// for TMEM on other SMs cannot block each other in a ring.
+
+constexpr int TM = 128;                 // rows of a tile; columns of y in a block
+constexpr int PK = 32;                  // columns of a panel (128 bytes of binary32)
+constexpr uint32_t PANEL = TM * 128;    // bytes of a panel of 128 rows
+
+__device__ __forceinline__ uint32_t swizzled(int row, int c16) { return (uint32_t)(row * 128 + ((c16 ^ (row & 7)) << 4)); }
+
+// Descriptor of a K-major operand in a swizzled panel: 8-row groups of 1024 bytes.
+__device__ __forceinline__ uint64_t panel_desc(uint32_t smem_addr) {
+    return (uint64_t)((smem_addr >> 4) & 0x3fffu) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+// kind::tf32, binary32 accumulator, both operands K-major, M x N.
+__host__ __device__ constexpr uint32_t idesc_tf32(int M, int N) {
+    return (1u << 4) | (2u << 7) | (2u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_tf32(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::tf32 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+}
+
+// The tf32 value nearest to v (ties away from zero), as binary32.
+__device__ __forceinline__ float tf32_near(float v) { return __uint_as_float((__float_as_uint(v) + 0x1000u) & 0xffffe000u); }
+
+// Four values as two tf32 parts, into the same place of two panels.
+__device__ __forceinline__ void store_split(char* hi, char* lo, uint32_t at, float4 v) {
+    const float4 h = make_float4(tf32_near(v.x), tf32_near(v.y), tf32_near(v.z), tf32_near(v.w));
+    *reinterpret_cast<float4*>(hi + at) = h;
+    *reinterpret_cast<float4*>(lo + at) =
+        make_float4(tf32_near(v.x - h.x), tf32_near(v.y - h.y), tf32_near(v.z - h.z), tf32_near(v.w - h.w));
+}
+
+// A thread's share of a panel of weights in flight: rows of 32 elements at a
+// pitch, 16 bytes at a time.
+template <class W>
+struct WeightPanel {
+    static constexpr bool SPLIT = sizeof(W) == 4;
+    static constexpr int EPU = 16 / (int)sizeof(W), UPR = PK / EPU, N = TM * UPR / THREADS;
+    uint4 q[N];
+    // rows and columns past the given ones are zeros
+    __device__ __forceinline__ void load(const W* src, int64_t pitch, int rows, int cols) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int u = i * THREADS + threadIdx.x, row = u / UPR, c = u % UPR;
+            q[i] = make_uint4(0, 0, 0, 0);
+            if (row < rows && c * EPU < cols) q[i] = __ldg(reinterpret_cast<const uint4*>(src + row * pitch + c * EPU));
+        }
+    }
+    // rows < `rows` (a multiple of 8) into the panel(s); lo: binary32 only
+    __device__ __forceinline__ void store(char* hi, char* lo, int rows) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int u = i * THREADS + threadIdx.x, row = u / UPR, c = u % UPR;
+            if (row >= rows) continue;
+            if constexpr (SPLIT) {
+                store_split(hi, lo, swizzled(row, c),
+                            make_float4(__uint_as_float(q[i].x), __uint_as_float(q[i].y), __uint_as_float(q[i].z),
+                                        __uint_as_float(q[i].w)));
+            } else {
+                float v[8];
+                unpack8(q[i], v, (const W*)nullptr);
+                *reinterpret_cast<float4*>(hi + swizzled(row, 2 * c)) = make_float4(v[0], v[1], v[2], v[3]);
+                *reinterpret_cast<float4*>(hi + swizzled(row, 2 * c + 1)) = make_float4(v[4], v[5], v[6], v[7]);
+            }
+        }
+    }
+};
+
+// Shared memory of the tile kernel, from a 1024-byte aligned start.
+//   step 1: two stages of x panel (hi, lo) and A panel (hi, and lo of binary32)
+//   step 2: partial sums at 0, u at `mid`
+//   step 3: panels of u (all hi, then all lo) at 0, two slots of B panel at `mid`
+struct TileSmem {
+    uint32_t wpanel, stage, mid, slot, total;
+    __host__ __device__ TileSmem(int r, bool split) {
+        const uint32_t panels = (uint32_t)(r + PK - 1) / PK;
+        wpanel = (uint32_t)((r + 15) / 16 * 16) * 128;
+        stage = 2 * PANEL + wpanel * (split ? 2 : 1);
+        mid = 2 * panels * PANEL;
+        slot = PANEL * (split ? 2 : 1);
+        const uint32_t u = TM * (uint32_t)(r + 4) * 4, tail = u > 2 * slot ? u : 2 * slot;
+        total = 2 * stage > mid + tail ? 2 * stage : mid + tail;
+    }
+};
+
+template <class W>
+__global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(THREADS, 2)
+    adapters_tile_kernel(const __grid_constant__ AdapterArgs p) {
+    constexpr bool SPLIT = WeightPanel<W>::SPLIT;
+    extern __shared__ char s_raw[];
+    __shared__ int s_tok[TM];
+    __shared__ int64_t s_off[2][TM];  // offsets of the rows of base and y
+    __shared__ uint64_t s_full[2], s_dfull[2];
+    __shared__ uint32_t s_tmem;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t rank = cluster_rank();
+    char* sm = s_raw + ((1024u - (smem_u32(s_raw) & 1023u)) & 1023u);
+    const uint32_t sa = smem_u32(sm);
+    const int r = p.r;
+    const TileSmem lay(r, SPLIT);
+
+    pdl_wait();
+    const int g = (int)(blockIdx.x / CL);
+    if (g >= *p.n_tiles) return;  // uniform over the cluster
+    const int4 tile = p.tiles[g];
+    const int id = tile.x, cnt = tile.z;
+    for (int i = tid; i < TM; i += THREADS) {
+        const int t = i < cnt ? p.perm[tile.y + i] : -1;
+        s_tok[i] = t;
+        s_off[0][i] = (int64_t)t * p.ldb;
+        s_off[1][i] = (int64_t)t * p.ldy;
+    }
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&s_dfull[i], 1);
+        }
+        mbar_fence_init();
+    }
+    __syncthreads();
+    if (id < 0) {  // no adapter (never in place: such rows have no tile then)
+        for (int t = (int)rank; t < cnt; t += CL)
+            for (int64_t n = tid; n < p.N; n += THREADS) p.y[s_off[1][t] + n] = p.base ? p.base[s_off[0][t] + n] : 0.0f;
+        return;
+    }
+    const W* a = static_cast<const W*>(p.a) + (int64_t)id * r * p.H;
+    const W* b = static_cast<const W*>(p.b) + (int64_t)id * p.N * r;
+    // every wait is bounded; one that gives up is reported and not repeated
+    bool alive = true;
+    const auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (alive && !mbar_wait_bounded(bar, parity, 1u << 22)) {
+            alive = false;
+            atomicOr(p.status, STATUS_SPIN_TIMEOUT);
+        }
+        tc_fence_after_sync();
+    };
+
+    // ---- 1: this CTA's part of u' over columns [h0, h0 + H / CL)
+    const uint32_t cols1 = r <= 32 ? 32u : r <= 64 ? 64u : 128u;
+    if (warp == 0) tmem_alloc(&s_tmem, cols1);
+    const int chunks = p.H / CL / PK, h0 = (int)rank * (p.H / CL);
+    const float* xr[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int t = s_tok[i * 32 + (tid >> 3)];
+        xr[i] = t < 0 ? nullptr : p.x + (int64_t)t * p.ldx + h0 + 4 * (tid & 7);
+    }
+    float4 xv[4];
+    WeightPanel<W> wv;
+    const auto load1 = [&](int c) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            xv[i] = xr[i] ? __ldg(reinterpret_cast<const float4*>(xr[i] + c * PK)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        wv.load(a + h0 + c * PK, p.H, r, PK);
+    };
+    load1(0);
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    uint32_t it = 0;  // panels handed to the tensor core so far, over steps 1 and 3
+    const int n16 = (r + 15) / 16 * 16;
+    for (int c = 0; c < chunks; ++c, ++it) {
+        const uint32_t st = it & 1;
+        if (it >= 2) wait(&s_full[st], ((it - 2) >> 1) & 1);
+        char* s = sm + st * lay.stage;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) store_split(s, s + PANEL, swizzled(i * 32 + (tid >> 3), tid & 7), xv[i]);
+        wv.store(s + 2 * PANEL, s + 2 * PANEL + lay.wpanel, r);
+        fence_proxy_async_smem();
+        __syncthreads();
+        if (tid == 0) {
+            tc_fence_after_sync();
+            const uint32_t s0 = sa + st * lay.stage;
+            const uint64_t xh = panel_desc(s0), xl = panel_desc(s0 + PANEL), wh = panel_desc(s0 + 2 * PANEL),
+                           wl = panel_desc(s0 + 2 * PANEL + lay.wpanel);
+#pragma unroll
+            for (int k = 0; k < PK / 8; ++k) {
+                mma_tf32(s_tmem, xh + 2 * k, wh + 2 * k, idesc_tf32(TM, n16), c + k > 0);
+                mma_tf32(s_tmem, xl + 2 * k, wh + 2 * k, idesc_tf32(TM, n16), true);
+                if (SPLIT) mma_tf32(s_tmem, xh + 2 * k, wl + 2 * k, idesc_tf32(TM, n16), true);
+            }
+            mma_commit(&s_full[st]);
+        }
+        if (c + 1 < chunks) load1(c + 1);
+    }
+    // this CTA's blocks of columns of y; the first panel of B travels while u is joined
+    const int64_t blocks = (p.N + TM - 1) / TM;
+    const int panels = (r + PK - 1) / PK;
+    const auto load3 = [&](int64_t nb, int k) {
+        wv.load(b + nb * TM * r + k * PK, r, (int)min((int64_t)TM, p.N - nb * TM), r - k * PK);
+    };
+    if ((int64_t)rank < blocks) load3(rank, 0);
+
+    // ---- 2: join the partial sums
+    wait(&s_full[(it - 1) & 1], ((it - 1) >> 1) & 1);
+    const int pitch = (r + 4) * 4;  // bytes of a row of partial sums and of u
+    for (int c = warp >> 2; c < r / 8; c += 2) {
+        uint32_t v[8];
+        tmem_ld8(s_tmem + (uint32_t)(((warp & 3) * 32) << 16) + 8u * c, v);
+        tmem_wait_ld();
+        float4* dst = reinterpret_cast<float4*>(sm + ((warp & 3) * 32 + lane) * pitch + 32 * c);
+        dst[0] = make_float4(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]), __uint_as_float(v[3]));
+        dst[1] = make_float4(__uint_as_float(v[4]), __uint_as_float(v[5]), __uint_as_float(v[6]), __uint_as_float(v[7]));
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    if (warp == 0) tmem_dealloc(s_tmem, cols1);
+    cluster_arrive();
+    cluster_wait();
+    const float scale = p.scale ? __ldg(p.scale + id) : 1.0f;
+    for (int i = tid; i < TM / CL * (r / 4); i += THREADS) {
+        const uint32_t at = (uint32_t)(((int)rank * (TM / CL) + i / (r / 4)) * pitch + i % (r / 4) * 16);
+        float4 part[CL];
+#pragma unroll
+        for (int c = 0; c < CL; ++c) part[c] = ld_cluster4(map_rank(sa + at, c));
+        float4 v = part[0];
+#pragma unroll
+        for (int c = 1; c < CL; ++c) {
+            v.x += part[c].x; v.y += part[c].y; v.z += part[c].z; v.w += part[c].w;
+        }
+        v.x *= scale; v.y *= scale; v.z *= scale; v.w *= scale;
+#pragma unroll
+        for (int c = 0; c < CL; ++c) st_cluster4(map_rank(sa + lay.mid + at, c), v);
+    }
+    cluster_arrive();
+    cluster_wait();
+    if ((int64_t)rank >= blocks) return;  // (no CTA reads or writes another's memory from here on)
+    // u as two tf32 parts in panels; row = row of the tile
+    if (warp == 0) tmem_alloc(&s_tmem, 2 * TM);
+    for (int i = tid; i < TM * (r / 4); i += THREADS) {
+        const int row = i / (r / 4), c = i % (r / 4);
+        store_split(sm + (c / 8) * PANEL, sm + (panels + c / 8) * PANEL, swizzled(row, c % 8),
+                    *reinterpret_cast<const float4*>(sm + lay.mid + row * pitch + 16 * c));
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+
+    // ---- 3: y = base + (B u^T)^T, block by block; MMAs of a block run under
+    // the epilogue of the block before it
+    const auto epilogue = [&](int64_t nb, uint32_t buf) {
+        const int64_t n = nb * TM + (warp & 3) * 32 + lane;
+        const uint32_t taddr = s_tmem + (uint32_t)(((warp & 3) * 32) << 16) + buf * TM;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+            const int t0 = (warp >> 2) * 64 + h * 32;
+            if (t0 >= cnt) break;
+            float bv[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                bv[j] = (t0 + j < cnt && n < p.N && p.base) ? p.base[s_off[0][t0 + j] + n] : 0.0f;
+            uint32_t v[32];
+            __syncwarp();
+            tmem_ld32(taddr + t0, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (t0 + j < cnt && n < p.N) p.y[s_off[1][t0 + j] + n] = bv[j] + __uint_as_float(v[j]);
+        }
+    };
+    uint32_t nd = 0;
+    for (int64_t nb = rank; nb < blocks; nb += CL, ++nd) {
+        for (int k = 0; k < panels; ++k, ++it) {
+            const uint32_t st = it & 1;
+            if (it >= 2) wait(&s_full[st], ((it - 2) >> 1) & 1);
+            char* s = sm + lay.mid + st * lay.slot;
+            wv.store(s, s + PANEL, TM);
+            fence_proxy_async_smem();
+            tc_fence_before_sync();
+            __syncthreads();
+            if (tid == 0) {
+                tc_fence_after_sync();
+                const uint32_t s0 = sa + lay.mid + st * lay.slot;
+                const uint64_t bh = panel_desc(s0), bl = panel_desc(s0 + PANEL), uh = panel_desc(sa + k * PANEL),
+                               ul = panel_desc(sa + (panels + k) * PANEL);
+                const uint32_t d = s_tmem + (nd & 1) * TM;
+                const int steps = min(PK, r - k * PK) / 8;
+                for (int j = 0; j < steps; ++j) {
+                    mma_tf32(d, bh + 2 * j, uh + 2 * j, idesc_tf32(TM, TM), k + j > 0);
+                    mma_tf32(d, bh + 2 * j, ul + 2 * j, idesc_tf32(TM, TM), true);
+                    if (SPLIT) mma_tf32(d, bl + 2 * j, uh + 2 * j, idesc_tf32(TM, TM), true);
+                }
+                mma_commit(&s_full[st]);
+                if (k == panels - 1) mma_commit(&s_dfull[nd & 1]);
+            }
+            if (k + 1 < panels)
+                load3(nb, k + 1);
+            else if (nb + CL < blocks)
+                load3(nb + CL, 0);
+        }
+        if (nd > 0) {
+            wait(&s_dfull[(nd - 1) & 1], ((nd - 1) >> 1) & 1);
+            epilogue(nb - CL, (nd - 1) & 1);
+        }
+    }
+    wait(&s_dfull[(nd - 1) & 1], ((nd - 1) >> 1) & 1);
+    epilogue((int64_t)rank + (int64_t)(nd - 1) * CL, (nd - 1) & 1);
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    if (warp == 0) tmem_dealloc(s_tmem, 2 * TM);
+}
+
 // ------------------------------------------------------------------ grouping
 
 // Group of id e: its adapter, or n for rows without one.
@@ -503,7 +855,22 @@ cudaError_t launch_rows(const AdapterArgs& p, const DeviceInfo& dev, cudaStream_
 }
 
 template <class W>
+cudaError_t launch_tiles(const AdapterArgs& p, cudaStream_t s) {
+    const TileSmem lay(p.r, sizeof(W) == 4);
+    const size_t smem = lay.total + 1024;
+    int per_sm = 0;  // (raises the kernel's shared-memory limit)
+    cudaError_t e = kernel_occupancy(reinterpret_cast<const void*>(adapters_tile_kernel<W>), THREADS, smem, &per_sm);
+    if (e != cudaSuccess) return e;
+    e = launch_group(p, TM, s);
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = p.T / TM + std::min<int64_t>(p.n + 1, p.T);
+    return launch_dependent(adapters_tile_kernel<W>, (unsigned)(tiles * CL), THREADS, smem, s, p);
+}
+
+// Tensor cores once adapters see enough rows to fill a good part of a tile.
+template <class W>
 cudaError_t launch_typed(const AdapterArgs& p, const DeviceInfo& dev, cudaStream_t s) {
+    if (p.T > INLINE_T && p.T >= (int64_t)TILE_MIN_ROWS * p.n) return launch_tiles<W>(p, s);
     return launch_rows<W>(p, dev, s);
 }
 
