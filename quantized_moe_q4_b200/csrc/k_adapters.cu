@@ -17,6 +17,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "launch.h"
@@ -61,6 +62,11 @@ __device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
 __device__ __forceinline__ void st_cluster4(uint32_t addr, float4 v) {
     asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
                  : "memory");
+}
+__device__ __forceinline__ int ld_cluster1(uint32_t addr) {
+    int v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
 }
 __device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
     float4 v;
@@ -321,45 +327,68 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(THREADS)
 //
 // Many rows: tiles of 128 rows of one adapter on the tensor cores, tf32 with
 // binary32 accumulators.  A binary32 value is split into two tf32 parts of 11
-// significant bits, v = hi + lo up to 2^-22 |v|; binary16 and bfloat16 weights
+// significant bits, v = hi + lo up to 2^-21 |v|; binary16 and bfloat16 weights
 // are tf32 values already, so a product with them takes two MMAs, and one of
 // two binary32 values three (lo * lo, 2^-22 of the product, is left out).
-//   1. u' = x A^T: each CTA of the cluster sums over its eighth of H.
-//      M = the tile's rows, N = r, operands K-major in 32-column panels with
-//      128-byte rows swizzled in 16-byte units (SWIZZLE_128B).
-//   2. the eight partial sums are joined through distributed shared memory:
-//      CTA c adds rows 16 c .. 16 c + 15 in rank order and hands them to all.
+//   1. u' = x A^T: each CTA of the cluster (of CLT = 1, 2, 4 or 8) sums over
+//      its part of H.  M = the tile's rows, N = r, operands K-major in
+//      32-column panels with 128-byte rows swizzled in 16-byte units
+//      (SWIZZLE_128B).  The tensor core truncates each sum, so a long chain of
+//      additions drifts: the panels take turns on several accumulators, the lo
+//      products have one of their own, and all are added in binary32.  (Error
+//      of y - base at H = 2048, r = 64, CLT = 1: 8.4e-7 of its norm; a plain
+//      binary32 product has 8.3e-7.)
+//   2. the partial sums are joined through distributed shared memory: each CTA
+//      adds its share of the rows in rank order and hands them to all.
 //   3. d^T = B u^T over the CTA's blocks of 128 columns of y: M = columns of y,
 //      N = the tile's rows, so that a TMEM lane is a column and every access
 //      of base and y is 32 consecutive floats, whatever their alignment.
 // TMEM is held inside steps 1 and 3 only, never across a cluster barrier: a
 // CTA that holds some waits for nothing but its own MMAs, so CTAs that wait
 // for TMEM on other SMs cannot block each other in a ring.
+//
+// A kernel that uses TMEM gets one CTA an SM here, so the CTA is wide and its
+// parts run apart: 16 warps convert x, join u and later read base and write y;
+// 3 warps bring the panels of A and, without waiting for u, of B, a panel a
+// warp; one issues the MMAs.  They meet on mbarriers only.
 
 constexpr int TM = 128;                 // rows of a tile; columns of y in a block
 constexpr int PK = 32;                  // columns of a panel (128 bytes of binary32)
 constexpr uint32_t PANEL = TM * 128;    // bytes of a panel of 128 rows
+constexpr int ROW_WARPS = 16, WEIGHT_WARPS = 3;  // (20 warps with the one of the MMAs: 96 registers a thread)
+constexpr int ROW_THREADS = 32 * ROW_WARPS;
+constexpr int TT = ROW_THREADS + 32 * WEIGHT_WARPS + 32;
+constexpr int AHEAD = 8;                // panels of x asked for ahead of the loads
+constexpr uint32_t COLS_TMEM = 512;
+constexpr int MAX_ACCS = 16;            // accumulators of the hi products in step 1, at most
 
 __device__ __forceinline__ uint32_t swizzled(int row, int c16) { return (uint32_t)(row * 128 + ((c16 ^ (row & 7)) << 4)); }
 
-// Descriptor of a K-major operand in a swizzled panel: 8-row groups of 1024 bytes.
-__device__ __forceinline__ uint64_t panel_desc(uint32_t smem_addr) {
-    return (uint64_t)((smem_addr >> 4) & 0x3fffu) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
-           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
+// Descriptor of a K-major operand in a swizzled panel (8-row groups of 1024
+// bytes): the low word; the high word is the same for all.
+__device__ __forceinline__ uint32_t panel_desc(uint32_t smem_addr) { return ((smem_addr >> 4) & 0x3fffu) | (1u << 16); }
+constexpr uint32_t PANEL_DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
 
 // kind::tf32, binary32 accumulator, both operands K-major, M x N.
 __host__ __device__ constexpr uint32_t idesc_tf32(int M, int N) {
     return (1u << 4) | (2u << 7) | (2u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-__device__ __forceinline__ void mma_tf32(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+__device__ __forceinline__ void mma_tf32(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+        "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::tf32 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        "tcgen05.mma.cta_group::1.kind::tf32 [%0], da, db, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(PANEL_DESC_HI)
         : "memory");
+}
+
+// One lane of a converged warp, the same at every call.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
 }
 
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
@@ -368,113 +397,178 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
                  : "r"(taddr)
                  : "memory");
 }
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
+__device__ __forceinline__ void arrive(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void sync_rows() { asm volatile("bar.sync 1, %0;" ::"n"(ROW_THREADS) : "memory"); }
 
 // The tf32 value nearest to v (ties away from zero), as binary32.
 __device__ __forceinline__ float tf32_near(float v) { return __uint_as_float((__float_as_uint(v) + 0x1000u) & 0xffffe000u); }
 
-// Four values as two tf32 parts, into the same place of two panels.
+// Four values as two tf32 parts, into the same place of two panels.  The lo
+// part (exact as a binary32 value, at most 2^-11 of v) is not rounded: the
+// MMA drops its low 13 bits, at most 2^-21 of v.
 __device__ __forceinline__ void store_split(char* hi, char* lo, uint32_t at, float4 v) {
     const float4 h = make_float4(tf32_near(v.x), tf32_near(v.y), tf32_near(v.z), tf32_near(v.w));
     *reinterpret_cast<float4*>(hi + at) = h;
-    *reinterpret_cast<float4*>(lo + at) =
-        make_float4(tf32_near(v.x - h.x), tf32_near(v.y - h.y), tf32_near(v.z - h.z), tf32_near(v.w - h.w));
+    *reinterpret_cast<float4*>(lo + at) = make_float4(v.x - h.x, v.y - h.y, v.z - h.z, v.w - h.w);
 }
 
-// A thread's share of a panel of weights in flight: rows of 32 elements at a
-// pitch, 16 bytes at a time.
+// Panels of B, the work of one warp: 16-byte units of a panel's rows are copied
+// as they are into a buffer of the warp's own (cp.async, so that a load's
+// latency passes under the panel before), and converted from there to tf32
+// values in the panel.  A lane reads the units that it copied itself.
 template <class W>
-struct WeightPanel {
+struct Panel {
     static constexpr bool SPLIT = sizeof(W) == 4;
-    static constexpr int EPU = 16 / (int)sizeof(W), UPR = PK / EPU, N = TM * UPR / THREADS;
-    uint4 q[N];
-    // rows and columns past the given ones are zeros
-    __device__ __forceinline__ void load(const W* src, int64_t pitch, int rows, int cols) {
+    static constexpr int EPU = 16 / (int)sizeof(W), UPR = PK / EPU;  // elements per unit, units per row
+    static constexpr int STEP = 32 / UPR;                            // rows that a warp covers at a time
+    static constexpr int BATCH = 512;                                // units per copy: a whole panel, or half of one
+    static constexpr int PARTS = TM * UPR / BATCH;
+    static constexpr uint32_t BYTES = 16 * BATCH;
+
+    // Start copying part `h` of a panel; rows from `have` and elements from
+    // `cols` on do not exist and are zeros.
+    __device__ __forceinline__ static void copy(const W* src, int64_t pitch, int have, int cols, int h, uint32_t raw) {
+        const int lane = threadIdx.x & 31, row0 = h * (BATCH / UPR) + lane / UPR, c = lane % UPR;
+        const bool col = c * EPU < cols;
+        const W* s = src + row0 * pitch + c * EPU;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int u = i * THREADS + threadIdx.x, row = u / UPR, c = u % UPR;
-            q[i] = make_uint4(0, 0, 0, 0);
-            if (row < rows && c * EPU < cols) q[i] = __ldg(reinterpret_cast<const uint4*>(src + row * pitch + c * EPU));
+        for (int j = 0; j < BATCH / 32; ++j, s += STEP * pitch) {
+            const bool there = col && row0 + j * STEP < have;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(raw + 16u * (32 * j + lane)),
+                         "l"(there ? s : src), "r"(there ? 16 : 0)
+                         : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    // Convert it (its copies have landed).
+    __device__ __forceinline__ static void convert(const char* raw, int h, char* hi) {
+        const int lane = threadIdx.x & 31, row0 = h * (BATCH / UPR) + lane / UPR, c = lane % UPR;
+#pragma unroll
+        for (int j = 0; j < BATCH / 32; ++j) {
+            const uint4 q = *reinterpret_cast<const uint4*>(raw + 16 * (32 * j + lane));
+            // (eight rows on is 1024 bytes on: the swizzle repeats)
+            store(q, swizzled(row0 + (j * STEP & 7), SPLIT ? c : 2 * c) + (uint32_t)(j * STEP / 8) * 1024u,
+                  swizzled(row0 + (j * STEP & 7), 2 * c + 1) + (uint32_t)(j * STEP / 8) * 1024u, hi);
         }
     }
-    // rows < `rows` (a multiple of 8) into the panel(s); lo: binary32 only
-    __device__ __forceinline__ void store(char* hi, char* lo, int rows) const {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int u = i * THREADS + threadIdx.x, row = u / UPR, c = u % UPR;
-            if (row >= rows) continue;
-            if constexpr (SPLIT) {
-                store_split(hi, lo, swizzled(row, c),
-                            make_float4(__uint_as_float(q[i].x), __uint_as_float(q[i].y), __uint_as_float(q[i].z),
-                                        __uint_as_float(q[i].w)));
-            } else {
-                float v[8];
-                unpack8(q[i], v, (const W*)nullptr);
-                *reinterpret_cast<float4*>(hi + swizzled(row, 2 * c)) = make_float4(v[0], v[1], v[2], v[3]);
-                *reinterpret_cast<float4*>(hi + swizzled(row, 2 * c + 1)) = make_float4(v[4], v[5], v[6], v[7]);
-            }
+    // One unit as tf32 values: at `at` of the hi and lo panels (binary32), or
+    // at `at` and `at2` of the panel.
+    __device__ __forceinline__ static void store(uint4 q, uint32_t at, uint32_t at2, char* hi) {
+        if constexpr (SPLIT) {
+            store_split(hi, hi + PANEL, at,
+                        make_float4(__uint_as_float(q.x), __uint_as_float(q.y), __uint_as_float(q.z), __uint_as_float(q.w)));
+        } else {
+            float v[8];
+            unpack8(q, v, (const W*)nullptr);
+            *reinterpret_cast<float4*>(hi + at) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4*>(hi + at2) = make_float4(v[4], v[5], v[6], v[7]);
         }
     }
 };
 
-// Shared memory of the tile kernel, from a 1024-byte aligned start.
-//   step 1: two stages of x panel (hi, lo) and A panel (hi, and lo of binary32)
-//   step 2: partial sums at 0, u at `mid`
-//   step 3: panels of u (all hi, then all lo) at 0, two slots of B panel at `mid`
+// Stages of step 1 (x and A) and slots of step 3 (panels of B).
+constexpr int stages_of(bool split) { return split ? 2 : 3; }
+
+// Shared memory of the tile kernel, from a 1024-byte aligned start: the slots
+// of B, at `raw` the weight warps' copies, then at `x`
+//   step 1: the stages: x (hi, lo panel) and A (binary32: hi, lo)
+//   step 2: partial sums at x, u at x + u
+//   step 3: panels of u (all hi, then all lo)
 struct TileSmem {
-    uint32_t wpanel, stage, mid, slot, total;
+    uint32_t slot, raw, x, u, total;
     __host__ __device__ TileSmem(int r, bool split) {
-        const uint32_t panels = (uint32_t)(r + PK - 1) / PK;
-        wpanel = (uint32_t)((r + 15) / 16 * 16) * 128;
-        stage = 2 * PANEL + wpanel * (split ? 2 : 1);
-        mid = 2 * panels * PANEL;
-        slot = PANEL * (split ? 2 : 1);
-        const uint32_t u = TM * (uint32_t)(r + 4) * 4, tail = u > 2 * slot ? u : 2 * slot;
-        total = 2 * stage > mid + tail ? 2 * stage : mid + tail;
+        slot = split ? 2 * PANEL : PANEL;
+        raw = stages_of(split) * slot;
+        x = raw + stages_of(split) * Panel<float>::BYTES;
+        u = TM * (uint32_t)(r + 4) * 4;
+        const uint32_t panels = (uint32_t)(r + PK - 1) / PK, stages = stages_of(split) * (2 * PANEL + slot);
+        uint32_t most = 2 * panels * PANEL > 2 * u ? 2 * panels * PANEL : 2 * u;
+        if (stages > most) most = stages;
+        total = x + most;
     }
 };
 
-template <class W>
-__global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(THREADS, 2)
-    adapters_tile_kernel(const __grid_constant__ AdapterArgs p) {
-    constexpr bool SPLIT = WeightPanel<W>::SPLIT;
+template <class W, int CLT>
+__global__ void __launch_bounds__(TT, 1) adapters_tile_kernel(const __grid_constant__ AdapterArgs p) {
+    constexpr bool SPLIT = sizeof(W) == 4;
+    constexpr uint32_t RING = stages_of(SPLIT);
     extern __shared__ char s_raw[];
     __shared__ int s_tok[TM];
-    __shared__ int64_t s_off[2][TM];  // offsets of the rows of base and y
-    __shared__ uint64_t s_full[2], s_dfull[2];
+    __shared__ __align__(16) int64_t s_off[2][TM];  // byte offsets of the rows of base and y (32-bit unless p.wide)
+    // stages full and empty again; slots of B full and empty again; blocks of y
+    // computed and read; the sums of step 1; u
+    __shared__ uint64_t s_full[RING], s_empty[RING], s_wfull[RING], s_wempty[RING], s_dfull[2], s_dempty[2], s_sums, s_u;
     __shared__ uint32_t s_tmem;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t rank = cluster_rank();
+    const uint32_t rank = CLT == 1 ? 0u : cluster_rank();
     char* sm = s_raw + ((1024u - (smem_u32(s_raw) & 1023u)) & 1023u);
     const uint32_t sa = smem_u32(sm);
     const int r = p.r;
     const TileSmem lay(r, SPLIT);
 
+    if (tid == 0) {
+        for (int i = 0; i < (int)RING; ++i) {
+            mbar_init(&s_full[i], ROW_WARPS / 2);
+            mbar_init(&s_empty[i], 1);
+            mbar_init(&s_wfull[i], 1);
+            mbar_init(&s_wempty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_dfull[i], 1);
+            mbar_init(&s_dempty[i], ROW_WARPS);
+        }
+        mbar_init(&s_sums, 1);
+        mbar_init(&s_u, ROW_WARPS);
+        mbar_fence_init();
+    }
     pdl_wait();
-    const int g = (int)(blockIdx.x / CL);
+    const int g = (int)(blockIdx.x / CLT);
     if (g >= *p.n_tiles) return;  // uniform over the cluster
     const int4 tile = p.tiles[g];
     const int id = tile.x, cnt = tile.z;
-    for (int i = tid; i < TM; i += THREADS) {
-        const int t = i < cnt ? p.perm[tile.y + i] : -1;
-        s_tok[i] = t;
-        s_off[0][i] = (int64_t)t * p.ldb;
-        s_off[1][i] = (int64_t)t * p.ldy;
-    }
-    if (tid == 0) {
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&s_full[i], 1);
-            mbar_init(&s_dfull[i], 1);
+    if (tid < TM) {
+        const int t = tid < cnt ? p.perm[tile.y + tid] : -1;
+        s_tok[tid] = t;
+        if (p.wide) {
+            s_off[0][tid] = 4 * (int64_t)t * p.ldb;
+            s_off[1][tid] = 4 * (int64_t)t * p.ldy;
+        } else {
+            reinterpret_cast<uint32_t*>(s_off[0])[tid] = 4u * (uint32_t)t * (uint32_t)p.ldb;
+            reinterpret_cast<uint32_t*>(s_off[1])[tid] = 4u * (uint32_t)t * (uint32_t)p.ldy;
         }
-        mbar_fence_init();
     }
     __syncthreads();
     if (id < 0) {  // no adapter (never in place: such rows have no tile then)
-        for (int t = (int)rank; t < cnt; t += CL)
-            for (int64_t n = tid; n < p.N; n += THREADS) p.y[s_off[1][t] + n] = p.base ? p.base[s_off[0][t] + n] : 0.0f;
+        constexpr int FLY = 16;
+        for (int t = (int)rank + CLT * warp; t < cnt; t += CLT * (TT / 32))
+            for (int64_t n = lane; n < p.N; n += 32 * FLY) {
+                const float* base = p.base + (int64_t)s_tok[t] * p.ldb + n;
+                float* y = p.y + (int64_t)s_tok[t] * p.ldy + n;
+                float v[FLY];
+#pragma unroll
+                for (int j = 0; j < FLY; ++j) v[j] = (p.base && n + 32 * j < p.N) ? base[32 * j] : 0.0f;
+#pragma unroll
+                for (int j = 0; j < FLY; ++j)
+                    if (n + 32 * j < p.N) y[32 * j] = v[j];
+            }
         return;
     }
-    const W* a = static_cast<const W*>(p.a) + (int64_t)id * r * p.H;
-    const W* b = static_cast<const W*>(p.b) + (int64_t)id * p.N * r;
+    if (warp == 0) tmem_alloc(&s_tmem, COLS_TMEM);
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
     // every wait is bounded; one that gives up is reported and not repeated
     bool alive = true;
     const auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -482,174 +576,365 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(THREADS, 2)
             alive = false;
             atomicOr(p.status, STATUS_SPIN_TIMEOUT);
         }
-        tc_fence_after_sync();
     };
-
-    // ---- 1: this CTA's part of u' over columns [h0, h0 + H / CL)
-    const uint32_t cols1 = r <= 32 ? 32u : r <= 64 ? 64u : 128u;
-    if (warp == 0) tmem_alloc(&s_tmem, cols1);
-    const int chunks = p.H / CL / PK, h0 = (int)rank * (p.H / CL);
-    const float* xr[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int t = s_tok[i * 32 + (tid >> 3)];
-        xr[i] = t < 0 ? nullptr : p.x + (int64_t)t * p.ldx + h0 + 4 * (tid & 7);
-    }
-    float4 xv[4];
-    WeightPanel<W> wv;
-    const auto load1 = [&](int c) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            xv[i] = xr[i] ? __ldg(reinterpret_cast<const float4*>(xr[i] + c * PK)) : make_float4(0.f, 0.f, 0.f, 0.f);
-        wv.load(a + h0 + c * PK, p.H, r, PK);
-    };
-    load1(0);
-    tc_fence_before_sync();
-    __syncthreads();
-    tc_fence_after_sync();
-    uint32_t it = 0;  // panels handed to the tensor core so far, over steps 1 and 3
-    const int n16 = (r + 15) / 16 * 16;
-    for (int c = 0; c < chunks; ++c, ++it) {
-        const uint32_t st = it & 1;
-        if (it >= 2) wait(&s_full[st], ((it - 2) >> 1) & 1);
-        char* s = sm + st * lay.stage;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) store_split(s, s + PANEL, swizzled(i * 32 + (tid >> 3), tid & 7), xv[i]);
-        wv.store(s + 2 * PANEL, s + 2 * PANEL + lay.wpanel, r);
-        fence_proxy_async_smem();
-        __syncthreads();
-        if (tid == 0) {
-            tc_fence_after_sync();
-            const uint32_t s0 = sa + st * lay.stage;
-            const uint64_t xh = panel_desc(s0), xl = panel_desc(s0 + PANEL), wh = panel_desc(s0 + 2 * PANEL),
-                           wl = panel_desc(s0 + 2 * PANEL + lay.wpanel);
-#pragma unroll
-            for (int k = 0; k < PK / 8; ++k) {
-                mma_tf32(s_tmem, xh + 2 * k, wh + 2 * k, idesc_tf32(TM, n16), c + k > 0);
-                mma_tf32(s_tmem, xl + 2 * k, wh + 2 * k, idesc_tf32(TM, n16), true);
-                if (SPLIT) mma_tf32(s_tmem, xh + 2 * k, wl + 2 * k, idesc_tf32(TM, n16), true);
-            }
-            mma_commit(&s_full[st]);
-        }
-        if (c + 1 < chunks) load1(c + 1);
-    }
-    // this CTA's blocks of columns of y; the first panel of B travels while u is joined
-    const int64_t blocks = (p.N + TM - 1) / TM;
-    const int panels = (r + PK - 1) / PK;
-    const auto load3 = [&](int64_t nb, int k) {
-        wv.load(b + nb * TM * r + k * PK, r, (int)min((int64_t)TM, p.N - nb * TM), r - k * PK);
-    };
-    if ((int64_t)rank < blocks) load3(rank, 0);
-
-    // ---- 2: join the partial sums
-    wait(&s_full[(it - 1) & 1], ((it - 1) >> 1) & 1);
-    const int pitch = (r + 4) * 4;  // bytes of a row of partial sums and of u
-    for (int c = warp >> 2; c < r / 8; c += 2) {
-        uint32_t v[8];
-        tmem_ld8(s_tmem + (uint32_t)(((warp & 3) * 32) << 16) + 8u * c, v);
-        tmem_wait_ld();
-        float4* dst = reinterpret_cast<float4*>(sm + ((warp & 3) * 32 + lane) * pitch + 32 * c);
-        dst[0] = make_float4(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]), __uint_as_float(v[3]));
-        dst[1] = make_float4(__uint_as_float(v[4]), __uint_as_float(v[5]), __uint_as_float(v[6]), __uint_as_float(v[7]));
-    }
-    tc_fence_before_sync();
-    __syncthreads();
-    tc_fence_after_sync();
-    if (warp == 0) tmem_dealloc(s_tmem, cols1);
-    cluster_arrive();
-    cluster_wait();
-    const float scale = p.scale ? __ldg(p.scale + id) : 1.0f;
-    for (int i = tid; i < TM / CL * (r / 4); i += THREADS) {
-        const uint32_t at = (uint32_t)(((int)rank * (TM / CL) + i / (r / 4)) * pitch + i % (r / 4) * 16);
-        float4 part[CL];
-#pragma unroll
-        for (int c = 0; c < CL; ++c) part[c] = ld_cluster4(map_rank(sa + at, c));
-        float4 v = part[0];
-#pragma unroll
-        for (int c = 1; c < CL; ++c) {
-            v.x += part[c].x; v.y += part[c].y; v.z += part[c].z; v.w += part[c].w;
-        }
-        v.x *= scale; v.y *= scale; v.z *= scale; v.w *= scale;
-#pragma unroll
-        for (int c = 0; c < CL; ++c) st_cluster4(map_rank(sa + lay.mid + at, c), v);
-    }
-    cluster_arrive();
-    cluster_wait();
-    if ((int64_t)rank >= blocks) return;  // (no CTA reads or writes another's memory from here on)
-    // u as two tf32 parts in panels; row = row of the tile
-    if (warp == 0) tmem_alloc(&s_tmem, 2 * TM);
-    for (int i = tid; i < TM * (r / 4); i += THREADS) {
-        const int row = i / (r / 4), c = i % (r / 4);
-        store_split(sm + (c / 8) * PANEL, sm + (panels + c / 8) * PANEL, swizzled(row, c % 8),
-                    *reinterpret_cast<const float4*>(sm + lay.mid + row * pitch + 16 * c));
-    }
-    tc_fence_before_sync();
-    __syncthreads();
-    tc_fence_after_sync();
-
-    // ---- 3: y = base + (B u^T)^T, block by block; MMAs of a block run under
-    // the epilogue of the block before it
-    const auto epilogue = [&](int64_t nb, uint32_t buf) {
-        const int64_t n = nb * TM + (warp & 3) * 32 + lane;
-        const uint32_t taddr = s_tmem + (uint32_t)(((warp & 3) * 32) << 16) + buf * TM;
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-            const int t0 = (warp >> 2) * 64 + h * 32;
-            if (t0 >= cnt) break;
-            float bv[32];
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-                bv[j] = (t0 + j < cnt && n < p.N && p.base) ? p.base[s_off[0][t0 + j] + n] : 0.0f;
-            uint32_t v[32];
+    const auto both_barriers = [&]() {  // of the roles that take no part in joining u
+        if constexpr (CLT > 1) {
             __syncwarp();
-            tmem_ld32(taddr + t0, v);
+            cluster_arrive();
+            cluster_wait();
+            cluster_arrive();
+            cluster_wait();
+        }
+    };
+    const int chunks = p.H / CLT / PK, h0 = (int)rank * (p.H / CLT);  // this CTA's part of H
+    const int64_t blocks = (p.N + TM - 1) / TM;                          // its blocks of y: rank, rank + CLT, ...
+    const int64_t mine = (int64_t)rank < blocks ? (blocks - rank + CLT - 1) / CLT : 0;
+    const int panels = (r + PK - 1) / PK, half = (panels + 1) / 2;       // of B; from `half` on a second accumulator
+    const int n16 = (r + 15) / 16 * 16;
+    const int accs = min(MAX_ACCS, (int)COLS_TMEM / n16 - 1);  // accumulators of the hi products; the lo ones' comes after them
+
+    if (warp >= ROW_WARPS + WEIGHT_WARPS) {
+        // ---------------- MMA (the whole warp waits, one lane issues)
+        const uint32_t xa = sa + lay.x;
+        const bool leader = elect_one();
+        uint32_t st = 0, ph = 0;  // stage or slot, and its phase
+        {
+            const uint32_t tmem = s_tmem, idesc = idesc_tf32(TM, n16), dl = tmem + (uint32_t)(accs * n16);
+            uint32_t dh = tmem;
+            for (int c = 0; c < chunks; ++c) {
+                wait(&s_full[st], ph);
+                tc_fence_after_sync();
+                const uint32_t xh = panel_desc(xa + st * (2 * PANEL + lay.slot)), xl = xh + (PANEL >> 4), wh = xl + (PANEL >> 4),
+                               wl = wh + (PANEL >> 4);
+                if (leader) {
+#pragma unroll
+                    for (int k = 0; k < PK / 8; ++k) {
+                        mma_tf32(dh, xh + 2 * k, wh + 2 * k, idesc, c >= accs || k > 0);
+                        mma_tf32(dl, xl + 2 * k, wh + 2 * k, idesc, c + k > 0);
+                        if (SPLIT) mma_tf32(dl, xh + 2 * k, wl + 2 * k, idesc, true);
+                    }
+                    mma_commit(&s_empty[st]);
+                }
+                __syncwarp();
+                dh = dh + n16 == dl ? tmem : dh + n16;
+                if (++st == RING) {
+                    st = 0;
+                    ph ^= 1;
+                }
+            }
+            if (leader) mma_commit(&s_sums);
+        }
+        both_barriers();
+        if (mine) {
+            wait(&s_u, 0);
+            tc_fence_after_sync();
+            const uint32_t tmem = s_tmem;
+            st = ph = 0;
+            for (int64_t i = 0; i < mine; ++i) {
+                const uint32_t buf = (uint32_t)i & 1;
+                if (i >= 2) wait(&s_dempty[buf], (uint32_t)((i >> 1) - 1) & 1);
+                for (int k = 0; k < panels; ++k) {
+                    wait(&s_wfull[st], ph);
+                    tc_fence_after_sync();
+                    const uint32_t bh = panel_desc(sa + st * lay.slot), bl = bh + (PANEL >> 4), uh = panel_desc(xa + k * PANEL),
+                                   ul = panel_desc(xa + (panels + k) * PANEL);
+                    if (leader) {
+                        const int steps = min(PK, r - k * PK) / 8;
+                        const uint32_t d = tmem + buf * 2 * TM + (k >= half ? TM : 0);
+                        for (int j = 0; j < steps; ++j) {  // the small products first
+                            mma_tf32(d, bh + 2 * j, ul + 2 * j, idesc_tf32(TM, TM), (k != 0 && k != half) || j > 0);
+                            if (SPLIT) mma_tf32(d, bl + 2 * j, uh + 2 * j, idesc_tf32(TM, TM), true);
+                        }
+                        for (int j = 0; j < steps; ++j) mma_tf32(d, bh + 2 * j, uh + 2 * j, idesc_tf32(TM, TM), true);
+                        mma_commit(&s_wempty[st]);
+                        if (k == panels - 1) mma_commit(&s_dfull[buf]);
+                    }
+                    __syncwarp();
+                    if (++st == RING) {
+                        st = 0;
+                        ph ^= 1;
+                    }
+                }
+            }
+        }
+        return;
+    }
+    if (warp >= ROW_WARPS) {
+        // ---------------- panels of B for each block of y, in the order of their
+        // use; panel q is warp q % RING's, so that a warp has a slot of its own
+        const uint32_t w = (uint32_t)(warp - ROW_WARPS);
+        if (w < RING) {
+            const W* b = static_cast<const W*>(p.b) + (int64_t)id * p.N * r;
+            char* slot = sm + w * lay.slot;
+            char* raw = sm + lay.raw + w * Panel<W>::BYTES;
+            struct Cursor {
+                int64_t i;  // block of y
+                int k, h;   // its panel, part of the panel
+            };
+            const auto step = [&](Cursor& c) {
+                if (++c.h < Panel<W>::PARTS) return;
+                c.h = 0;
+                for (c.k += (int)RING; c.k >= panels; c.k -= panels) ++c.i;
+            };
+            const auto copy = [&](const Cursor& c) {
+                if (c.i >= mine) return;
+                const int64_t n0 = ((int64_t)rank + c.i * CLT) * TM;
+                Panel<W>::copy(b + n0 * r + c.k * PK, r, (int)min((int64_t)TM, p.N - n0), r - c.k * PK, c.h, smem_u32(raw));
+                // the base under the block is needed soon after
+                if (c.k == 0 && c.h == 0 && p.base)
+                    for (int t = lane; t < cnt; t += 32) {
+                        const float* row = p.base + (int64_t)s_tok[t] * p.ldb + n0;
+#pragma unroll
+                        for (int o = 0; o < TM; o += 32)
+                            if (n0 + o < p.N) prefetch_l2(row + o);
+                    }
+            };
+            Cursor at = {0, (int)w, 0};
+            for (; at.k >= panels; at.k -= panels) ++at.i;
+            copy(at);
+            uint32_t n = 0;  // panels that this warp has brought
+            for (; at.i < mine; ++n) {
+                if (n == 1) both_barriers();  // (the slot's first panel waits for u; so must this warp)
+                if (n > 0) wait(&s_wempty[w], (n - 1) & 1);
+#pragma unroll
+                for (int h = 0; h < Panel<W>::PARTS; ++h) {
+                    asm volatile("cp.async.wait_group 0;" ::: "memory");
+                    Panel<W>::convert(raw, h, slot);
+                    step(at);
+                    copy(at);  // over what was just read, by the same lanes
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) arrive(&s_wfull[w]);
+            }
+            if (n < 2) both_barriers();
+        } else {
+            both_barriers();
+        }
+        return;
+    }
+
+    // ---------------- rows
+    // 1: x as two tf32 parts.  Two groups of 8 warps take the chunks in turn (a
+    // warp's own chain of instructions is what takes its time, not the SM's
+    // rates); thread t of a group has 16 bytes of rows t / 8 + 32 i of a panel.
+    constexpr int GROUP = ROW_THREADS / 2, PER = TM * 8 / GROUP, FLY = 2;
+    const int gt = tid % GROUP, first = tid / GROUP;
+    const float* xr[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int t = s_tok[i * (GROUP / 8) + (gt >> 3)];
+        xr[i] = t < 0 ? nullptr : p.x + (int64_t)t * p.ldx + h0 + 4 * (gt & 7);
+    }
+    // thread i of a group asks for the line of row i of its panels
+    const float* xp = gt < TM && s_tok[gt] >= 0 ? p.x + (int64_t)s_tok[gt] * p.ldx + h0 : nullptr;
+    if (xp)
+        for (int c = first; c < AHEAD && c < chunks; c += 2) prefetch_l2(xp + c * PK);
+    // ... and units gt + GROUP i of the panel of A
+    constexpr int UPR = Panel<W>::UPR, EPU = Panel<W>::EPU, WPER = TM * UPR / GROUP;
+    const W* wr = static_cast<const W*>(p.a) + ((int64_t)id * r + gt / UPR) * p.H + h0 + gt % UPR * EPU;
+    const uint32_t wrows = (uint32_t)(GROUP / UPR);
+    float4 xv[FLY][PER];
+    uint4 wv[FLY][WPER];
+    const auto load_x = [&](int c, float4 (&v)[PER], uint4 (&w)[WPER]) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            v[i] = xr[i] ? __ldg(reinterpret_cast<const float4*>(xr[i] + c * PK)) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < WPER; ++i)
+            if (gt / UPR + i * wrows < (uint32_t)r) w[i] = __ldg(reinterpret_cast<const uint4*>(wr + (int64_t)i * wrows * p.H + c * PK));
+    };
+    uint32_t st = (uint32_t)first, ph = 1;  // (a stage is empty at first)
+    const uint32_t at0 = swizzled(gt >> 3, gt & 7);  // (32 rows on: the same swizzle)
+    const uint32_t wat = swizzled(gt / UPR, gt % UPR * (Panel<W>::SPLIT ? 1 : 2)), wat2 = swizzled(gt / UPR, gt % UPR * 2 + 1);
+    const auto put_x = [&](int c, float4 (&v)[PER], uint4 (&w)[WPER]) {
+        if (c >= (int)RING) wait(&s_empty[st], ph);
+        char* s = sm + lay.x + st * (2 * PANEL + lay.slot);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) store_split(s, s + PANEL, at0 + i * (GROUP / 8) * 128, v[i]);
+#pragma unroll
+        for (int i = 0; i < WPER; ++i)
+            if (gt / UPR + i * wrows < (uint32_t)r)
+                Panel<W>::store(w[i], wat + i * wrows * 128, wat2 + i * wrows * 128, s + 2 * PANEL);
+        if (c + 2 * FLY < chunks) load_x(c + 2 * FLY, v, w);
+        if (xp && c + AHEAD < chunks) prefetch_l2(xp + (c + AHEAD) * PK);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) arrive(&s_full[st]);
+        st += 2;
+        if (st >= RING) {
+            st -= RING;
+            ph ^= 1;
+        }
+    };
+#pragma unroll
+    for (int j = 0; j < FLY; ++j)
+        if (first + 2 * j < chunks) load_x(first + 2 * j, xv[j], wv[j]);
+    for (int c = first; c < chunks; c += 2 * FLY) {
+#pragma unroll
+        for (int j = 0; j < FLY; ++j)
+            if (c + 2 * j < chunks) put_x(c + 2 * j, xv[j], wv[j]);
+    }
+
+    // 2: u
+    const float scale = p.scale ? __ldg(p.scale + id) : 1.0f;
+    const int pitch = (r + 4) * 4;  // bytes of a row of partial sums and of u
+    char* xs = sm + lay.x;
+    const int quad = warp & 3;      // the TMEM lanes that this warp reads are 32 quad .. + 31
+    wait(&s_sums, 0);
+    tc_fence_after_sync();
+    for (int c = warp >> 2; c < r / 8; c += ROW_WARPS / 4) {
+        const uint32_t at = s_tmem + (uint32_t)((quad * 32) << 16) + 8u * c;
+        float sum[8];
+        uint32_t v[8];
+        tmem_ld8(at + (uint32_t)(accs * n16), v);  // the small products first
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[j] = __uint_as_float(v[j]);
+        for (int q = 0; q < accs && q < chunks; ++q) {
+            tmem_ld8(at + (uint32_t)(q * n16), v);
             tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (t0 + j < cnt && n < p.N) p.y[s_off[1][t0 + j] + n] = bv[j] + __uint_as_float(v[j]);
+            for (int j = 0; j < 8; ++j) sum[j] += __uint_as_float(v[j]);
         }
-    };
-    uint32_t nd = 0;
-    for (int64_t nb = rank; nb < blocks; nb += CL, ++nd) {
-        for (int k = 0; k < panels; ++k, ++it) {
-            const uint32_t st = it & 1;
-            if (it >= 2) wait(&s_full[st], ((it - 2) >> 1) & 1);
-            char* s = sm + lay.mid + st * lay.slot;
-            wv.store(s, s + PANEL, TM);
-            fence_proxy_async_smem();
-            tc_fence_before_sync();
-            __syncthreads();
-            if (tid == 0) {
-                tc_fence_after_sync();
-                const uint32_t s0 = sa + lay.mid + st * lay.slot;
-                const uint64_t bh = panel_desc(s0), bl = panel_desc(s0 + PANEL), uh = panel_desc(sa + k * PANEL),
-                               ul = panel_desc(sa + (panels + k) * PANEL);
-                const uint32_t d = s_tmem + (nd & 1) * TM;
-                const int steps = min(PK, r - k * PK) / 8;
-                for (int j = 0; j < steps; ++j) {
-                    mma_tf32(d, bh + 2 * j, uh + 2 * j, idesc_tf32(TM, TM), k + j > 0);
-                    mma_tf32(d, bh + 2 * j, ul + 2 * j, idesc_tf32(TM, TM), true);
-                    if (SPLIT) mma_tf32(d, bl + 2 * j, uh + 2 * j, idesc_tf32(TM, TM), true);
-                }
-                mma_commit(&s_full[st]);
-                if (k == panels - 1) mma_commit(&s_dfull[nd & 1]);
-            }
-            if (k + 1 < panels)
-                load3(nb, k + 1);
-            else if (nb + CL < blocks)
-                load3(nb + CL, 0);
-        }
-        if (nd > 0) {
-            wait(&s_dfull[(nd - 1) & 1], ((nd - 1) >> 1) & 1);
-            epilogue(nb - CL, (nd - 1) & 1);
+        const int row = quad * 32 + lane;
+        const float4 lo4 = make_float4(sum[0], sum[1], sum[2], sum[3]), hi4 = make_float4(sum[4], sum[5], sum[6], sum[7]);
+        if constexpr (CLT == 1) {
+            char* h = xs + (c / 4) * PANEL;
+            char* l = xs + (panels + c / 4) * PANEL;
+            store_split(h, l, swizzled(row, c % 4 * 2), make_float4(lo4.x * scale, lo4.y * scale, lo4.z * scale, lo4.w * scale));
+            store_split(h, l, swizzled(row, c % 4 * 2 + 1), make_float4(hi4.x * scale, hi4.y * scale, hi4.z * scale, hi4.w * scale));
+        } else {
+            float4* dst = reinterpret_cast<float4*>(xs + row * pitch + 32 * c);
+            dst[0] = lo4;
+            dst[1] = hi4;
         }
     }
-    wait(&s_dfull[(nd - 1) & 1], ((nd - 1) >> 1) & 1);
-    epilogue((int64_t)rank + (int64_t)(nd - 1) * CL, (nd - 1) & 1);
+    if constexpr (CLT > 1) {
+        tc_fence_before_sync();
+        sync_rows();
+        tc_fence_after_sync();
+        if (warp == 0) tmem_dealloc(s_tmem, COLS_TMEM);
+        cluster_arrive();
+        cluster_wait();
+        const uint32_t xa = sa + lay.x;
+        for (int i = tid; i < TM / CLT * (r / 4); i += ROW_THREADS) {
+            const uint32_t at = (uint32_t)(((int)rank * (TM / CLT) + i / (r / 4)) * pitch + i % (r / 4) * 16);
+            float4 part[CLT];
+#pragma unroll
+            for (int c = 0; c < CLT; ++c) part[c] = ld_cluster4(map_rank(xa + at, c));
+            float4 v = part[0];
+#pragma unroll
+            for (int c = 1; c < CLT; ++c) {
+                v.x += part[c].x; v.y += part[c].y; v.z += part[c].z; v.w += part[c].w;
+            }
+            v.x *= scale; v.y *= scale; v.z *= scale; v.w *= scale;
+#pragma unroll
+            for (int c = 0; c < CLT; ++c) st_cluster4(map_rank(xa + lay.u + at, c), v);
+        }
+        cluster_arrive();
+        cluster_wait();
+        if (!mine) return;  // (no CTA reads or writes another's memory from here on)
+        if (warp == 0) tmem_alloc(&s_tmem, COLS_TMEM);
+        // from rows of u to panels, which lie over them
+        constexpr int MOST = TM * (128 / 4) / ROW_THREADS;
+        float4 v[MOST];
+#pragma unroll
+        for (int j = 0; j < MOST; ++j) {
+            const int i = j * ROW_THREADS + tid, row = i / (r / 4), c = i % (r / 4);
+            if (row < TM) v[j] = *reinterpret_cast<const float4*>(xs + lay.u + row * pitch + 16 * c);
+        }
+        sync_rows();
+#pragma unroll
+        for (int j = 0; j < MOST; ++j) {
+            const int i = j * ROW_THREADS + tid, row = i / (r / 4), c = i % (r / 4);
+            if (row < TM) store_split(xs + (c / 8) * PANEL, xs + (panels + c / 8) * PANEL, swizzled(row, c % 8), v[j]);
+        }
+    }
+    fence_proxy_async_smem();
     tc_fence_before_sync();
-    __syncthreads();
+    __syncwarp();
+    if (lane == 0) arrive(&s_u);
+
+    // 3: y = base + d.  Warp w has columns 32 (w % 4) .. + 31 of a block, a lane
+    // a column, and rows 32 (w / 4) .. + 31, in two halves: while one is added
+    // and written, the base of the other and of the next block is on its way.
+    // Offsets of rows are 32-bit byte offsets unless the buffers are larger
+    // (one add an access instead of three), and a full half is done without
+    // predicates.
+    const int t0 = (warp >> 2) * 32;
+    const int rows = cnt - t0;  // may be <= 0 or > 32
+    const auto finish = [&](auto wide) {
+        using Off = std::conditional_t<decltype(wide)::value, int64_t, uint32_t>;
+        const Off* boff = reinterpret_cast<const Off*>(s_off[0]) + t0;
+        const Off* yoff = reinterpret_cast<const Off*>(s_off[1]) + t0;
+        const char* base = reinterpret_cast<const char*>(p.base);
+        char* y = reinterpret_cast<char*>(p.y);
+        float bv[2][16];
+        const auto load_base = [&](int64_t i, int h) {
+            const int64_t n = ((int64_t)rank + i * CLT) * TM + quad * 32 + lane;
+            if (!base) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) bv[h][j] = 0.0f;
+            } else if (rows >= 16 * h + 16 && n - lane + 32 <= p.N) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) bv[h][j] = *reinterpret_cast<const float*>(base + (Off)(boff[16 * h + j] + 4 * (Off)n));
+            } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (16 * h + j < rows && n < p.N)
+                        bv[h][j] = *reinterpret_cast<const float*>(base + (Off)(boff[16 * h + j] + 4 * (Off)n));
+            }
+        };
+        load_base(0, 0);
+        load_base(0, 1);
+        for (int64_t i = 0; i < mine; ++i) {
+            const uint32_t buf = (uint32_t)i & 1;
+            const int64_t n = ((int64_t)rank + i * CLT) * TM + quad * 32 + lane;
+            wait(&s_dfull[buf], (uint32_t)(i >> 1) & 1);
+            tc_fence_after_sync();
+            __syncwarp();
+            const uint32_t at = s_tmem + (uint32_t)((quad * 32) << 16) + buf * 2 * TM + t0;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t v[16];
+                tmem_ld16(at + 16 * h, v);
+                tmem_wait_ld();
+                if (panels > 1) {
+                    uint32_t v2[16];
+                    tmem_ld16(at + TM + 16 * h, v2);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(v2[j]));
+                }
+                if (h == 1) {
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) arrive(&s_dempty[buf]);
+                }
+                if (rows >= 16 * h + 16 && n - lane + 32 <= p.N) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        *reinterpret_cast<float*>(y + (Off)(yoff[16 * h + j] + 4 * (Off)n)) = bv[h][j] + __uint_as_float(v[j]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (16 * h + j < rows && n < p.N)
+                            *reinterpret_cast<float*>(y + (Off)(yoff[16 * h + j] + 4 * (Off)n)) = bv[h][j] + __uint_as_float(v[j]);
+                }
+                if (i + 1 < mine) load_base(i + 1, h);
+                __syncwarp();
+            }
+        }
+    };
+    if (p.wide)
+        finish(std::true_type{});
+    else
+        finish(std::false_type{});
+    tc_fence_before_sync();
+    sync_rows();
     tc_fence_after_sync();
-    if (warp == 0) tmem_dealloc(s_tmem, 2 * TM);
+    if (warp == 0) tmem_dealloc(s_tmem, COLS_TMEM);
 }
 
 // ------------------------------------------------------------------ grouping
@@ -687,8 +972,10 @@ __device__ __forceinline__ void rank_ids(const int32_t* ids, int64_t first, int6
 
 // Offsets of the groups in perm and of their tiles in the tile list
 // (exclusive sums over n + 1 groups, the rows without an adapter last), and
-// the tile list itself.  cnt, off, toff: shared arrays of MAX_ADAPTERS + 2.
-__device__ __forceinline__ void scan_groups(const AdapterArgs& p, int tile_rows, const int* cnt, int* off, int* toff) {
+// this CTA's share (part of parts) of the tile list.  cnt, off, toff: shared
+// arrays of MAX_ADAPTERS + 2.
+__device__ __forceinline__ void scan_groups(const AdapterArgs& p, int tile_rows, const int* cnt, int* off, int* toff, int part,
+                                            int parts) {
     __shared__ unsigned long long s_warp[GROUP_THREADS / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int c = tid < p.n ? cnt[tid] : 0;
@@ -724,11 +1011,11 @@ __device__ __forceinline__ void scan_groups(const AdapterArgs& p, int tile_rows,
         off[p.n] = (int)(incl >> 32);
         toff[p.n] = (int)(incl & 0xffffffffu);
         toff[p.n + 1] = toff[p.n] + none;
-        *p.n_tiles = toff[p.n + 1];
+        if (part == 0) *p.n_tiles = toff[p.n + 1];
     }
     __syncthreads();
     const int tiles = toff[p.n + 1];
-    for (int i = tid; i < tiles; i += GROUP_THREADS) {
+    for (int i = part * GROUP_THREADS + tid; i < tiles; i += parts * GROUP_THREADS) {
         int lo = 0, hi = p.n;  // the last group whose tiles start at or before i
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
@@ -739,21 +1026,53 @@ __device__ __forceinline__ void scan_groups(const AdapterArgs& p, int tile_rows,
     }
 }
 
-// Up to GROUP_CHUNK rows: one CTA does it all.
-__global__ void __launch_bounds__(GROUP_THREADS) adapters_group_kernel(const __grid_constant__ AdapterArgs p, int tile_rows) {
-    __shared__ int cnt[MAX_ADAPTERS + 2], off[MAX_ADAPTERS + 2], toff[MAX_ADAPTERS + 2];
+// Up to CLG * GROUP_CHUNK rows in one launch of one cluster: each CTA counts
+// `per` rows, the counts are added through distributed shared memory, each
+// CTA places its own rows.
+template <int CLG>
+__global__ void __launch_bounds__(GROUP_THREADS)
+    adapters_group_kernel(const __grid_constant__ AdapterArgs p, int tile_rows, int per) {
+    __shared__ int cnt[MAX_ADAPTERS + 2], all[MAX_ADAPTERS + 2], off[MAX_ADAPTERS + 2], toff[MAX_ADAPTERS + 2];
     pdl_launch_dependents();
+    const int rank = CLG == 1 ? 0 : (int)cluster_rank();
+    const int64_t first = (int64_t)rank * per, last = CLG == 1 ? p.T : min(p.T, first + per);
     for (int i = threadIdx.x; i < p.n + 2; i += GROUP_THREADS) cnt[i] = 0;
     __syncthreads();
     int grp[GROUP_IDS], rnk[GROUP_IDS];
     bool bad = false;
-    rank_ids(p.ids, 0, p.T, p.n, cnt, grp, rnk, bad);
-    const int any = __syncthreads_or(bad);
-    scan_groups(p, tile_rows, cnt, off, toff);
+    rank_ids(p.ids, first, last, p.n, cnt, grp, rnk, bad);
+    if (bad) cnt[p.n + 1] = 1;
+    if constexpr (CLG == 1) {
+        __syncthreads();
+        scan_groups(p, tile_rows, cnt, off, toff, 0, 1);
+    } else {
+        cluster_arrive();
+        cluster_wait();
+        // totals; and this CTA's rows of a group come after those of the CTAs before it
+        for (int i = threadIdx.x; i < p.n + 2; i += GROUP_THREADS) {
+            int sum = 0, before = 0;
+#pragma unroll
+            for (int c = 0; c < CLG; ++c) {
+                const int v = ld_cluster1(map_rank(smem_u32(&cnt[i]), c));
+                before += c < rank ? v : 0;
+                sum += v;
+            }
+            all[i] = sum;
+            toff[i] = before;
+        }
+        cluster_arrive();
+        cluster_wait();  // (every CTA has read the counts)
+        for (int i = threadIdx.x; i < p.n + 1; i += GROUP_THREADS) cnt[i] = toff[i];
+        __syncthreads();
+        scan_groups(p, tile_rows, all, off, toff, rank, CLG);
+        for (int i = threadIdx.x; i < p.n + 1; i += GROUP_THREADS) off[i] += cnt[i];
+        __syncthreads();
+    }
 #pragma unroll
     for (int i = 0; i < GROUP_IDS; ++i)
-        if (grp[i] >= 0) p.perm[off[grp[i]] + rnk[i]] = i * GROUP_THREADS + threadIdx.x;
-    if (threadIdx.x == 0) *p.status = any ? STATUS_BAD_ADAPTER_INDEX : 0u;
+        if (grp[i] >= 0) p.perm[off[grp[i]] + rnk[i]] = (int32_t)(first + i * GROUP_THREADS + threadIdx.x);
+    const int* total = CLG == 1 ? cnt : all;
+    if (rank == 0 && threadIdx.x == 0) *p.status = total[p.n + 1] ? STATUS_BAD_ADAPTER_INDEX : 0u;
 }
 
 // More rows: counts per chunk, offsets of every (chunk, group), placement.
@@ -779,7 +1098,7 @@ __global__ void __launch_bounds__(GROUP_THREADS)
         cnt[i] = c;
     }
     __syncthreads();
-    scan_groups(p, tile_rows, cnt, off, toff);
+    scan_groups(p, tile_rows, cnt, off, toff, 0, 1);
     for (int i = threadIdx.x; i < p.n + 1; i += GROUP_THREADS) {
         int at = off[i];
         for (int k = 0; k < nchunks; ++k) {
@@ -805,33 +1124,42 @@ __global__ void __launch_bounds__(GROUP_THREADS) adapters_place_kernel(const __g
         if (grp[i] >= 0) p.perm[at[grp[i]] + rnk[i]] = (int32_t)(first + i * GROUP_THREADS + threadIdx.x);
 }
 
-cudaError_t launch_group(const AdapterArgs& p, int tile_rows, cudaStream_t s) {
-    const int nchunks = (int)ceil_div(p.T, GROUP_CHUNK);
-    if (nchunks == 1) {
-        adapters_group_kernel<<<1, GROUP_THREADS, 0, s>>>(p, tile_rows);
-        return cudaGetLastError();
-    }
-    adapters_count_kernel<<<nchunks, GROUP_THREADS, 0, s>>>(p);
-    adapters_scan_kernel<<<1, GROUP_THREADS, 0, s>>>(p, nchunks, tile_rows);
-    adapters_place_kernel<<<nchunks, GROUP_THREADS, 0, s>>>(p);
-    return cudaGetLastError();
-}
-
-// A launch that may begin while the kernel before it drains (its kernels wait
-// with pdl_wait before they read anything).
+// A launch of clusters of `cluster` CTAs; dependent: it may begin while the
+// kernel before it drains (its kernels wait with pdl_wait before they read
+// anything).
 template <class... A>
-cudaError_t launch_dependent(void (*kernel)(A...), unsigned grid, int threads, size_t smem, cudaStream_t s, A... args) {
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
+cudaError_t launch_clusters(void (*kernel)(A...), unsigned grid, int cluster, int threads, size_t smem, bool dependent,
+                            cudaStream_t s, A... args) {
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = dependent ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+cudaError_t launch_group(const AdapterArgs& p, int tile_rows, cudaStream_t s) {
+    if (p.T <= 2 * GROUP_THREADS) {
+        adapters_group_kernel<1><<<1, GROUP_THREADS, 0, s>>>(p, tile_rows, 0);
+        return cudaGetLastError();
+    }
+    if (p.T <= (int64_t)CL * GROUP_CHUNK) {
+        const int per = (int)ceil_div(ceil_div(p.T, CL), GROUP_THREADS) * GROUP_THREADS;
+        return launch_clusters(adapters_group_kernel<CL>, CL, CL, GROUP_THREADS, 0, false, s, p, tile_rows, per);
+    }
+    const int nchunks = (int)ceil_div(p.T, GROUP_CHUNK);
+    adapters_count_kernel<<<nchunks, GROUP_THREADS, 0, s>>>(p);
+    adapters_scan_kernel<<<1, GROUP_THREADS, 0, s>>>(p, nchunks, tile_rows);
+    adapters_place_kernel<<<nchunks, GROUP_THREADS, 0, s>>>(p);
+    return cudaGetLastError();
 }
 
 template <class W>
@@ -851,27 +1179,42 @@ cudaError_t launch_rows(const AdapterArgs& p, const DeviceInfo& dev, cudaStream_
     }
     cudaError_t e = launch_group(p, ROWS, s);
     if (e != cudaSuccess) return e;
-    return launch_dependent(adapters_rows_kernel<W, false>, (unsigned)grid, THREADS, 0, s, p, (int)chunks, (int)iters);
+    return launch_clusters(adapters_rows_kernel<W, false>, (unsigned)grid, CL, THREADS, 0, true, s, p, (int)chunks, (int)iters);
 }
 
-template <class W>
+template <class W, int CLT>
 cudaError_t launch_tiles(const AdapterArgs& p, cudaStream_t s) {
     const TileSmem lay(p.r, sizeof(W) == 4);
     const size_t smem = lay.total + 1024;
     int per_sm = 0;  // (raises the kernel's shared-memory limit)
-    cudaError_t e = kernel_occupancy(reinterpret_cast<const void*>(adapters_tile_kernel<W>), THREADS, smem, &per_sm);
+    cudaError_t e = kernel_occupancy(reinterpret_cast<const void*>(adapters_tile_kernel<W, CLT>), TT, smem, &per_sm);
     if (e != cudaSuccess) return e;
     e = launch_group(p, TM, s);
     if (e != cudaSuccess) return e;
     const int64_t tiles = p.T / TM + std::min<int64_t>(p.n + 1, p.T);
-    return launch_dependent(adapters_tile_kernel<W>, (unsigned)(tiles * CL), THREADS, smem, s, p);
+    return launch_clusters(adapters_tile_kernel<W, CLT>, (unsigned)(tiles * CLT), CLT, TT, smem, true, s, p);
 }
 
-// Tensor cores once adapters see enough rows to fill a good part of a tile.
+// The choice of kernel.  Tiles pay off once adapters see enough rows to fill
+// a good part of one.  CLT: the tile kernel has one CTA an SM, so the widest
+// cluster that still runs all tiles at once (about 12 of 13 SMs can hold
+// clusters of 4, and 15 clusters of 8 fit); but wide enough that an
+// accumulator of step 1 sums no more than CHAIN panels, since each addition
+// truncates (4 CHAIN additions drift by about 1e-6 of the sum).
 template <class W>
 cudaError_t launch_typed(const AdapterArgs& p, const DeviceInfo& dev, cudaStream_t s) {
-    if (p.T > INLINE_T && p.T >= (int64_t)TILE_MIN_ROWS * p.n) return launch_tiles<W>(p, s);
-    return launch_rows<W>(p, dev, s);
+    constexpr int CHAIN = 10;
+    const int n16 = (p.r + 15) / 16 * 16, accs = std::min(MAX_ACCS, (int)COLS_TMEM / n16 - 1), chunks = p.H / PK;
+    if (p.T <= INLINE_T || p.T < (int64_t)TILE_MIN_ROWS * p.n || chunks > CL * accs * CHAIN) return launch_rows<W>(p, dev, s);
+    // adapters with a tile each while they see fewer rows than a tile has, else half a tile too many each
+    const int64_t tiles = p.T < (int64_t)TM * (p.n + 1) ? std::min<int64_t>(p.T, p.n + 1) : p.T / TM + (p.n + 1) / 2;
+    const auto fits = [&](int c) { return tiles * c <= (c <= 2 ? dev.sm_count : c == 4 ? dev.sm_count * 12 / 13 : 15 * dev.sm_count / 148 * 8); };
+    const auto short_enough = [&](int c) { return chunks <= c * accs * CHAIN; };
+    { const char* e = getenv("CLT"); const int c = e ? atoi(e) : 0; if (c) return c == 1 ? launch_tiles<W, 1>(p, s) : c == 2 ? launch_tiles<W, 2>(p, s) : c == 4 ? launch_tiles<W, 4>(p, s) : launch_tiles<W, 8>(p, s); }
+    if (fits(8) || !short_enough(4)) return launch_tiles<W, 8>(p, s);
+    if (fits(4) || !short_enough(2)) return launch_tiles<W, 4>(p, s);
+    if (fits(2) || !short_enough(1)) return launch_tiles<W, 2>(p, s);
+    return launch_tiles<W, 1>(p, s);
 }
 
 }  // namespace
@@ -896,7 +1239,9 @@ size_t adapters_layout(int n, int64_t T, char* base, AdapterArgs* p) {
     return off[5];
 }
 
-cudaError_t launch_adapters(const AdapterArgs& p, int dtype, const DeviceInfo& dev, cudaStream_t s) {
+cudaError_t launch_adapters(const AdapterArgs& args, int dtype, const DeviceInfo& dev, cudaStream_t s) {
+    AdapterArgs p = args;
+    p.wide = 4 * (p.T * std::max(p.ldb, p.ldy) + p.N) > 0xffffffffll;
     if (dtype == 0) return launch_typed<float>(p, dev, s);
     if (dtype == 1) return launch_typed<__half>(p, dev, s);
     return launch_typed<__nv_bfloat16>(p, dev, s);

@@ -148,6 +148,7 @@ struct AdapterArgs {
     float* y;
     int64_t ldx, ldb, ldy, N, T;
     int H, r, n;
+    int wide;            // byte offsets in base or y pass 32 bits (set by launch_adapters)
     // workspace
     uint32_t* status;
     int32_t* n_tiles;
