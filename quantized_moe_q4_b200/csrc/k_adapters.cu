@@ -1205,6 +1205,7 @@ template <class W>
 cudaError_t launch_typed(const AdapterArgs& p, const DeviceInfo& dev, cudaStream_t s) {
     constexpr int CHAIN = 10;
     const int n16 = (p.r + 15) / 16 * 16, accs = std::min(MAX_ACCS, (int)COLS_TMEM / n16 - 1), chunks = p.H / PK;
+    if (getenv("ROWS")) return launch_rows<W>(p, dev, s);
     if (p.T <= INLINE_T || p.T < (int64_t)TILE_MIN_ROWS * p.n || chunks > CL * accs * CHAIN) return launch_rows<W>(p, dev, s);
     // adapters with a tile each while they see fewer rows than a tile has, else half a tile too many each
     const int64_t tiles = p.T < (int64_t)TM * (p.n + 1) ? std::min<int64_t>(p.T, p.n + 1) : p.T / TM + (p.n + 1) / 2;

@@ -6,14 +6,21 @@
 // Mixture-of-Experts Model on a 6GB 2011 GPU", Dutch technical summary,
 // Resultaten) is moe_q4_gemv here, and this is what follows it.
 //
-// One pass over the logits: a row is the work of one cluster, whose CTAs own
-// consecutive slices of the vocabulary.  The sparse parts become dense in
-// shared memory first -- a 32-bit word per token of the slice that counts its
-// occurrences in the row's history -- while the slice's logits are already on
-// their way into registers; then every logit is read once, ruled, written
-// once if asked for, and enters a running (maximum, lowest index, sum of
-// exponentials), which the cluster joins through distributed shared memory.
+// A row is the work of one cluster.  Its CTAs own the vocabulary's groups of 32
+// tokens in turn (the tokens that histories are full of have low numbers, and
+// would all fall to one CTA if each owned a range).  While the logits are on
+// their way to L2, the few that penalties and biases change are worked out in
+// shared memory: a 32-bit word per token counts its occurrences in the row's
+// history, a list keeps the tokens that occur, their ruled logits replace
+// their counts, and a bit per token says where that was done.  Then the logits
+// are streamed once: four of them cost one test of four bits, the mask, a
+// running maximum and, relative to the warp's maximum, one exponential each.
+// The CTAs' (maximum, lowest token, sum) are joined through distributed shared
+// memory.  Bound by the logits' bytes (read, and written if asked for); CTAs
+// are small, so that four of them an SM cover one another's latencies.
 #include <algorithm>
+#include <atomic>
+#include <type_traits>
 
 #include "common.cuh"
 #include "launch.h"
@@ -23,13 +30,13 @@ namespace moeq4 {
 
 namespace {
 
-constexpr int THREADS = 512;
+constexpr int THREADS = 256;
 constexpr int WARPS = THREADS / 32;
-constexpr int MAX_CL = 8;           // CTAs per cluster (the portable limit)
-constexpr int VEC = 4;              // logits per access
-constexpr int BATCH = 8;            // accesses in flight per thread
-constexpr int STEP = THREADS * VEC * BATCH;  // logits a CTA holds at a time
-constexpr int MAX_SLICE = 32768;    // logits whose words fit the shared memory (128 KB)
+constexpr int MAX_CL = 16;          // CTAs per cluster (beyond 8: not portable, allowed on sm_100a)
+constexpr int BATCH = 8;            // 16-byte accesses in flight per thread
+constexpr int STEP = THREADS * 4 * BATCH;  // logits a CTA holds at a time
+constexpr int FIRST_CTAS = 592;     // CTAs that ask for the lists of all rows (about the first to run)
+constexpr int MAX_SLICE = 4 * STEP;  // logits whose words and list fit the shared memory (200 KB)
 
 // History word of a token: bit 31: it occurs in the prompt; low bits: times generated.
 constexpr uint32_t IN_PROMPT = 0x80000000u;
@@ -40,18 +47,38 @@ struct Best {
     float s;   // sum of exp(l - m); NaN where a logit is NaN
 };
 
-// exp(v - m) with m >= v; equal infinities give 1, -inf gives 0.
-__device__ __forceinline__ float exp_below(float v, float m) { return v == m ? 1.0f : __expf(v - m); }
+// exp(d) for d <= 0 (relative error 2^-22 + |d| 2^-23; below 2^-126: 0).
+__device__ __forceinline__ float exp_neg(float d) {
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(d * 1.4426950408889634f));
+    return e;
+}
 
+// exp(v - m) for m >= v, equal infinities included.
+__device__ __forceinline__ float exp_below(float v, float m) { return v == m ? 1.0f : exp_neg(v - m); }
+
+// (a side without anything has s = 0, or NaN, which has to stay)
 __device__ __forceinline__ Best join(Best a, Best b) {
-    const bool take = b.m > a.m || (b.m == a.m && b.i < a.i);
     Best r;
     r.m = fmaxf(a.m, b.m);
-    r.i = take ? b.i : a.i;
-    // a side without anything has s = 0 (or NaN, which has to stay)
-    r.s = (a.m == r.m ? a.s : a.s * exp_below(a.m, r.m)) + (b.m == r.m ? b.s : b.s * exp_below(b.m, r.m));
+    r.i = b.m > a.m ? b.i : b.m < a.m ? a.i : min(a.i, b.i);
+    r.s = a.s * exp_below(a.m, r.m) + b.s * exp_below(b.m, r.m);
     return r;
 }
+
+// Joins the first n (a power of two) lanes' values into lane 0, in a fixed order.
+__device__ __forceinline__ Best join_lanes(Best b, int n) {
+    for (int o = n / 2; o > 0; o >>= 1) {
+        Best c;
+        c.m = __shfl_down_sync(0xffffffffu, b.m, o);
+        c.i = __shfl_down_sync(0xffffffffu, b.i, o);
+        c.s = __shfl_down_sync(0xffffffffu, b.s, o);
+        b = join(b, c);
+    }
+    return b;
+}
+
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 struct Row {
     float rep, pres, freq;
@@ -69,44 +96,86 @@ __device__ __forceinline__ float penalise(float l, uint32_t word, const Row& r) 
 
 __device__ __forceinline__ int64_t clamp64(int64_t v, int64_t lo, int64_t hi) { return v < lo ? lo : v > hi ? hi : v; }
 
-// f(token, position) for the entries [lo, hi) of an int32 list.
+// f(token, position) for the entries [lo, hi) of an int32 list, 16-byte loads
+// from the last aligned position at or before lo, four of them in flight.
 template <class F>
 __device__ __forceinline__ void each_token(const int32_t* list, int64_t lo, int64_t hi, F f) {
-    // 16-byte loads from the last aligned position at or before lo
-    for (int64_t i = (lo & ~int64_t(3)) + 4 * threadIdx.x; i < hi; i += 4 * THREADS) {
-        if (i >= lo && i + 4 <= hi) {
-            const int4 q = __ldg(reinterpret_cast<const int4*>(list + i));
-            f(q.x, i); f(q.y, i + 1); f(q.z, i + 2); f(q.w, i + 3);
-        } else {
-            for (int k = 0; k < 4; ++k)
-                if (i + k >= lo && i + k < hi) f(__ldg(list + i + k), i + k);
+    constexpr int FLY = 4;
+    for (int64_t i0 = (lo & ~int64_t(3)) + 4 * threadIdx.x; i0 < hi; i0 += 4 * THREADS * FLY) {
+        int4 q[FLY];
+#pragma unroll
+        for (int j = 0; j < FLY; ++j) {
+            const int64_t i = i0 + 4 * THREADS * j;
+            if (i >= lo && i + 4 <= hi) {
+                q[j] = __ldg(reinterpret_cast<const int4*>(list + i));
+            } else {  // (-1 is no token)
+                q[j].x = i >= lo && i < hi ? __ldg(list + i) : -1;
+                q[j].y = i + 1 >= lo && i + 1 < hi ? __ldg(list + i + 1) : -1;
+                q[j].z = i + 2 >= lo && i + 2 < hi ? __ldg(list + i + 2) : -1;
+                q[j].w = i + 3 >= lo && i + 3 < hi ? __ldg(list + i + 3) : -1;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < FLY; ++j) {
+            const int64_t i = i0 + 4 * THREADS * j;
+            f(q[j].x, i); f(q[j].y, i + 1); f(q[j].z, i + 2); f(q[j].w, i + 3);
         }
     }
 }
 
-// Dynamic shared memory: words[slice] (history word, or for a biased token
-// the bits of its logit after penalties and bias), then biased[slice / 32]
-// (bit set: the word is such a logit).  `slice` is a multiple of 32.
-__global__ void __launch_bounds__(THREADS, 2) logits_kernel(const __grid_constant__ LogitArgs p, int slice) {
+// Dynamic shared memory: allowed[slice / 32] (the mask's words), and for rows
+// with histories or biases words[slice] (history word, or for a ruled token
+// the bits of its logit), ruled[slice / 32] (bit set: the word is such a
+// logit), listed[slice / 32] (bit set: a bias lists the token), seen[slice]
+// (16-bit: the tokens of the history, once each).  Place i of a CTA's `slice`
+// (a multiple of 32) is token base + 32 * (i / 32 * ncl + rank) + i % 32, with
+// ncl = 1 << lg CTAs in the cluster.
+__global__ void __launch_bounds__(THREADS, 4) logits_kernel(const __grid_constant__ LogitArgs p, int slice, int lg) {
     extern __shared__ __align__(16) uint32_t s_mem[];
     __shared__ Best s_best[WARPS];
     __shared__ Best s_cl[MAX_CL];
-    __shared__ int s_dup;
+    __shared__ int s_dup, s_seen;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    uint32_t rank, ncl;
+    uint32_t rank;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ncl));
-    const int64_t t = blockIdx.x / ncl;
+    const int64_t t = blockIdx.x >> lg;
     const bool pick = p.token || p.lse;
     const float NEG = __int_as_float(0xff800000);
     if (pick) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    uint32_t* words = s_mem;
-    uint32_t* biased = s_mem + slice;
+    uint32_t* words = s_mem + (p.mask ? (slice / 32 + 3) / 4 * 4 : 0);
+    uint32_t* ruled = words + slice;
+    uint32_t* listed = ruled + slice / 32;
+    uint16_t* seen = reinterpret_cast<uint16_t*>(listed + slice / 32);
+    const float* in = p.logits + t * p.ld;
+    float* out = p.out ? p.out + t * p.ldo : nullptr;
+    const auto token_at = [&](uint32_t i) { return (((i >> 5 << lg) + rank) << 5) + (i & 31); };  // less base
 
-    Row row;
-    row.rep = p.rep ? __ldg(p.rep + t) : 1.0f;
-    row.pres = p.pres ? __ldg(p.pres + t) : 0.0f;
-    row.freq = p.freq ? __ldg(p.freq + t) : 0.0f;
+    // What the rules need comes through a chain of dependent loads, which a
+    // busy memory makes long: the logits are asked for before it begins, and
+    // the lists of all rows by the first CTAs, a share each.
+    const bool ruling = p.row_start || p.bias_start || p.mask;
+    if (ruling) {
+        for (int g = tid; g < slice / 32; g += THREADS) {
+            const uint32_t v = token_at(32 * g);
+            if (v < p.V) prefetch_l2(in + v);
+        }
+        if (blockIdx.x < FIRST_CTAS) {
+            const int64_t c = (int64_t)blockIdx.x * THREADS + tid, all = (int64_t)min(gridDim.x, (unsigned)FIRST_CTAS) * THREADS;
+            if (p.row_start) {
+                for (int64_t i = 32 * c; i < p.n_tokens; i += 32 * all) prefetch_l2(p.tokens + i);
+                for (int64_t i = 16 * c; i < p.T; i += 16 * all) {
+                    prefetch_l2(p.row_start + i);
+                    if (p.generated) prefetch_l2(p.generated + i);
+                }
+            }
+            if (p.bias_start)
+                for (int64_t i = 32 * c; i < p.n_bias; i += 32 * all) {
+                    prefetch_l2(p.bias_token + i);
+                    prefetch_l2(p.bias_value + i);
+                }
+        }
+    }
+
     int64_t h0 = 0, h1 = 0, hg = 0, b0 = 0, b1 = 0;
     if (p.row_start) {
         h0 = clamp64(__ldg(p.row_start + t), 0, p.n_tokens);
@@ -117,7 +186,6 @@ __global__ void __launch_bounds__(THREADS, 2) logits_kernel(const __grid_constan
         b0 = clamp64(__ldg(p.bias_start + t), 0, p.n_bias);
         b1 = clamp64(__ldg(p.bias_start + t + 1), b0, p.n_bias);
     }
-    const bool dense = h1 > h0 || b1 > b0;
     // the row's mask: none, or a row of words; an index outside the masks
     // allows nothing
     const uint32_t* mask = nullptr;
@@ -131,145 +199,249 @@ __global__ void __launch_bounds__(THREADS, 2) logits_kernel(const __grid_constan
             if (tid == 0 && rank == 0 && p.status) atomicOr(p.status, STATUS_BAD_MASK_INDEX);
         }
     }
-    const float* in = p.logits + t * p.ld;
-    float* out = p.out ? p.out + t * p.ldo : nullptr;
     const bool vec = (reinterpret_cast<uintptr_t>(in) & 15) == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0;
     Best best{NEG, 0x7fffffff, 0.0f};
 
-    for (int64_t v0 = (int64_t)rank * slice; v0 < p.V; v0 += (int64_t)ncl * slice) {
-        const int len = (int)min((int64_t)slice, p.V - v0);
-        for (int s0 = 0; s0 < len; s0 += STEP) {
-            // logits of this step: access j of thread tid covers tokens
-            // s0 + (j * THREADS + tid) * VEC + 0..3 of the slice
-            float l[BATCH][VEC];
-#pragma unroll
-            for (int j = 0; j < BATCH; ++j) {
-                const int i = s0 + (j * THREADS + tid) * VEC;
-                if (vec && i + VEC <= len) {
-                    const float4 q = *reinterpret_cast<const float4*>(in + v0 + i);
-                    l[j][0] = q.x; l[j][1] = q.y; l[j][2] = q.z; l[j][3] = q.w;
-                } else {
-#pragma unroll
-                    for (int k = 0; k < VEC; ++k) l[j][k] = i + k < len ? in[v0 + i + k] : NEG;
-                }
-            }
-            if (s0 == 0 && dense) {
-                __syncthreads();  // (an earlier slice's words are done with)
-                for (int i = tid; i < (len + 3) / 4; i += THREADS) reinterpret_cast<uint4*>(words)[i] = make_uint4(0, 0, 0, 0);
-                if (b1 > b0)
-                    for (int i = tid; i < (len + 31) / 32; i += THREADS) biased[i] = 0;
-                if (tid == 0) s_dup = 0;
+    for (int64_t base = 0; base < p.V; base += (int64_t)slice << lg) {
+        const int left = (int)min(p.V - base, (int64_t)slice << lg);  // tokens of this turn, of all CTAs
+        // this CTA's places: `len` with all of its last group; the group may end early
+        const int groups = (left + 31) / 32, len = max(0, groups - (int)rank + (1 << lg) - 1 >> lg) * 32;
+        const float* src = in + base;
+        float* dst = out + base;
+        const bool sparse = h1 > h0 || b1 > b0;
+        if (sparse || mask) {
+            // ---- the mask's words, and what penalties and biases change: worked
+            // out before anything is written (outputs may be in place)
+            const auto inside = [&](int v, uint32_t& i) {  // (vocabularies end at 2^30)
+                const uint32_t u = (uint32_t)v - (uint32_t)base, g = u >> 5;
+                i = (g >> lg << 5) + (u & 31);
+                return u < (uint32_t)left && (g & ((1u << lg) - 1)) == rank;
+            };
+            __syncthreads();  // (an earlier turn's words are done with)
+            if (mask)
+                for (int g = tid; g < len / 32; g += THREADS) s_mem[g] = __ldg(mask + (base >> 5) + (((uint32_t)g << lg) + rank));
+            if (sparse) {
+                Row row;
+                row.rep = p.rep ? __ldg(p.rep + t) : 1.0f;
+                row.pres = p.pres ? __ldg(p.pres + t) : 0.0f;
+                row.freq = p.freq ? __ldg(p.freq + t) : 0.0f;
+                if (h1 > h0)
+                    for (int i = tid; i < len / 4; i += THREADS) reinterpret_cast<uint4*>(words)[i] = make_uint4(0, 0, 0, 0);
+                for (int i = tid; i < len / 32; i += THREADS) ruled[i] = listed[i] = 0;
+                if (tid == 0) s_dup = s_seen = 0;
                 __syncthreads();
                 each_token(p.tokens, h0, h1, [&](int v, int64_t at) {
-                    const int64_t i = (int64_t)v - v0;
-                    if (i < 0 || i >= len || v < 0) return;
+                    uint32_t i;
+                    if (!inside(v, i)) return;
+                    const uint32_t bit = 1u << (i & 31);
                     if (at >= hg) atomicAdd(&words[i], 1u);
-                    else atomicOr(&words[i], IN_PROMPT);
+                    else if (!(words[i] & IN_PROMPT)) atomicOr(&words[i], IN_PROMPT);
+                    if (!(ruled[i >> 5] & bit) && !(atomicOr(&ruled[i >> 5], bit) & bit)) seen[atomicAdd(&s_seen, 1)] = (uint16_t)i;
                 });
+                for (int64_t e = b0 + tid; e < b1; e += THREADS) {
+                    uint32_t i;
+                    if (!inside(__ldg(p.bias_token + e), i)) continue;
+                    const uint32_t bit = 1u << (i & 31);
+                    if (atomicOr(&listed[i >> 5], bit) & bit) s_dup = 1;
+                }
+                __syncthreads();
+                const int n = s_seen;
+#pragma unroll 4
+                for (int e = tid; e < n; e += THREADS) {
+                    const int i = seen[e];
+                    words[i] = __float_as_uint(penalise(src[token_at(i)], words[i], row));
+                }
                 if (b1 > b0) {
-                    for (int64_t e = b0 + tid; e < b1; e += THREADS) {
-                        const int64_t i = (int64_t)__ldg(p.bias_token + e) - v0;
-                        if (i < 0 || i >= len) continue;
-                        const uint32_t bit = 1u << (i & 31);
-                        if (atomicOr(&biased[i >> 5], bit) & bit) s_dup = 1;
-                    }
                     __syncthreads();
                     for (int64_t e = b0 + tid; e < b1; e += THREADS) {
                         const int v = __ldg(p.bias_token + e);
-                        const int64_t i = (int64_t)v - v0;
-                        if (i < 0 || i >= len) continue;
+                        uint32_t i;
+                        if (!inside(v, i)) continue;
                         bool last = true;  // the later entry of a token listed twice counts
                         if (s_dup)
                             for (int64_t f = e + 1; f < b1 && last; ++f) last = __ldg(p.bias_token + f) != v;
-                        if (last)
-                            words[i] = __float_as_uint(__fadd_rn(penalise(in[v0 + i], words[i], row), __ldg(p.bias_value + e)));
+                        if (!last) continue;
+                        const uint32_t bit = 1u << (i & 31);
+                        const float l = atomicOr(&ruled[i >> 5], bit) & bit ? __uint_as_float(words[i]) : src[token_at(i)];
+                        words[i] = __float_as_uint(__fadd_rn(l, __ldg(p.bias_value + e)));
                     }
                 }
-                __syncthreads();  // (with outputs in place, nothing is written before this)
             }
-            float top = NEG;
-            bool nan = false;
+            __syncthreads();
+        }
+
+        // ---- Up to STEP logits from place s0 on.  Vectors: access j of a thread
+        // covers its places s0 + (j * THREADS + tid) * 4 + 0 .. 3; else places
+        // s0 + (4 j + k) * THREADS + tid, so that a warp's 32 are one group.
+        // FULL: all of them exist.
+        const auto stream = [&](auto vector, auto full, int s0) {
+            constexpr bool VECTOR = decltype(vector)::value, FULL = decltype(full)::value;
+            const int i0 = s0 + (VECTOR ? 4 * tid : tid);
+            // its first logit's token (less base), and how much further the next access's is
+            const int v0 = (int)token_at(i0), step = (VECTOR ? 4 * THREADS : THREADS) << lg;
+            const auto exist = [&](int j) { return left - (v0 + j * step); };  // (vectors) of access j's logits; may be <= 0 or > 4
+            const float* q0 = src + v0;
+            float* d0 = dst + v0;
+            float l[BATCH][4];
 #pragma unroll
             for (int j = 0; j < BATCH; ++j) {
-                const int i = s0 + (j * THREADS + tid) * VEC;
-                if (i >= len) continue;
-                uint32_t allowed = 0xfu;
-                if (mask) allowed = __ldg(mask + ((v0 + i) >> 5)) >> (i & 31);
-                if (nothing) allowed = 0;
-                if (dense) {
-                    const uint4 q = *reinterpret_cast<const uint4*>(words + i);
-                    const uint32_t w[VEC] = {q.x, q.y, q.z, q.w};
-                    const uint32_t over = b1 > b0 ? biased[i >> 5] >> (i & 31) : 0u;
-#pragma unroll
-                    for (int k = 0; k < VEC; ++k)
-                        l[j][k] = (over >> k) & 1u ? __uint_as_float(w[k]) : penalise(l[j][k], w[k], row);
-                }
-#pragma unroll
-                for (int k = 0; k < VEC; ++k) {
-                    if (!((allowed >> k) & 1u)) l[j][k] = NEG;
-                    if (i + k < len) {
-                        top = fmaxf(top, l[j][k]);
-                        nan |= l[j][k] != l[j][k];
-                    }
-                }
-                if (out) {
-                    if (vec && i + VEC <= len) {
-                        *reinterpret_cast<float4*>(out + v0 + i) = make_float4(l[j][0], l[j][1], l[j][2], l[j][3]);
+                if constexpr (VECTOR) {
+                    const float* q = q0 + (int64_t)j * step;
+                    if (FULL || exist(j) >= 4) {
+                        const float4 f = *reinterpret_cast<const float4*>(q);
+                        l[j][0] = f.x; l[j][1] = f.y; l[j][2] = f.z; l[j][3] = f.w;
                     } else {
 #pragma unroll
-                        for (int k = 0; k < VEC; ++k)
-                            if (i + k < len) out[v0 + i + k] = l[j][k];
+                        for (int k = 0; k < 4; ++k) l[j][k] = k < exist(j) ? q[k] : NEG;
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) l[j][k] = FULL || exist(4 * j + k) > 0 ? q0[(int64_t)(4 * j + k) * step] : NEG;
+                }
+            }
+            float top = NEG;
+#pragma unroll
+            for (int j = 0; j < BATCH; ++j) {
+                if (!FULL && exist(VECTOR ? j : 4 * j) <= 0) continue;
+                if constexpr (VECTOR) {
+                    const int i = i0 + j * 4 * THREADS;
+                    if (sparse) {
+                        const uint32_t over = ruled[i >> 5] >> (i & 31) & 0xfu;
+                        if (over) {
+                            const uint4 q = *reinterpret_cast<const uint4*>(words + i);
+                            if (over & 1u) l[j][0] = __uint_as_float(q.x);
+                            if (over & 2u) l[j][1] = __uint_as_float(q.y);
+                            if (over & 4u) l[j][2] = __uint_as_float(q.z);
+                            if (over & 8u) l[j][3] = __uint_as_float(q.w);
+                        }
+                    }
+                    if (mask) {
+                        const uint32_t allowed = s_mem[i >> 5] >> (i & 31);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (!(allowed & (1u << k))) l[j][k] = NEG;
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int i = i0 + (4 * j + k) * THREADS;
+                        if (!FULL && exist(4 * j + k) <= 0) continue;
+                        if (sparse && (ruled[i >> 5] >> lane) & 1u) l[j][k] = __uint_as_float(words[i]);
+                        if (mask && !((s_mem[i >> 5] >> lane) & 1u)) l[j][k] = NEG;
+                    }
+                }
+                if (nothing)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) l[j][k] = NEG;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) top = fmaxf(top, l[j][k]);  // (ignores NaN; what does not exist is -inf)
+                if (out) {
+                    if constexpr (VECTOR) {
+                        float* q = d0 + (int64_t)j * step;
+                        if (FULL || exist(j) >= 4) {
+                            *reinterpret_cast<float4*>(q) = make_float4(l[j][0], l[j][1], l[j][2], l[j][3]);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (k < exist(j)) q[k] = l[j][k];
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (FULL || exist(4 * j + k) > 0) d0[(int64_t)(4 * j + k) * step] = l[j][k];
                     }
                 }
             }
-            if (!pick) continue;
-            if (nan) best.s = __int_as_float(0x7fffffff);
-            if (top == NEG) continue;
-            Best b{top, 0x7fffffff, 0.0f};
+            if (!pick) return;
+            // the warp's maximum, then sums relative to it
+            float m = top;
 #pragma unroll
-            for (int j = 0; j < BATCH; ++j) {
-                const int i = s0 + (j * THREADS + tid) * VEC;
+            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            Best b{m, 0x7fffffff, 0.0f};
+            if (fabsf(m) != __int_as_float(0x7f800000)) {
+                float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int k = 0; k < VEC; ++k)
-                    if (i + k < len && l[j][k] == l[j][k]) {
-                        b.s += exp_below(l[j][k], top);
-                        if (l[j][k] == top) b.i = min(b.i, (int)(v0 + i + k));
-                    }
+                for (int j = 0; j < BATCH; ++j)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) s[k] += exp_neg(l[j][k] - m);
+                b.s = (s[0] + s[1]) + (s[2] + s[3]);
+            } else {
+                // nothing (every logit -inf or NaN), or an infinite maximum
+#pragma unroll
+                for (int j = 0; j < BATCH; ++j)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) b.s += l[j][k] == m ? (m > 0.0f ? 1.0f : 0.0f) : l[j][k] != l[j][k] ? l[j][k] : 0.0f;
+            }
+            if (top == m && m != NEG) {
+#pragma unroll
+                for (int j = 0; j < BATCH; ++j)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (l[j][k] == m) b.i = min(b.i, (int)base + v0 + (VECTOR ? j * step + k : (4 * j + k) * step));
             }
             best = join(best, b);
+        };
+        // (a turn's groups are complete but for its very last)
+        const int whole = left & 31 ? len - 32 : len;
+        for (int s0 = 0; s0 < len; s0 += STEP) {
+            if (vec && s0 + STEP <= whole)
+                stream(std::true_type{}, std::true_type{}, s0);
+            else if (vec)
+                stream(std::true_type{}, std::false_type{}, s0);
+            else if (s0 + STEP <= whole)
+                stream(std::false_type{}, std::true_type{}, s0);
+            else
+                stream(std::false_type{}, std::false_type{}, s0);
         }
     }
     if (!pick) return;
-    // warp, CTA, cluster: always in the same order
+    // warp (all lanes have the same maximum here), CTA, cluster: always in the
+    // same order
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-        Best b;
-        b.m = __shfl_down_sync(0xffffffffu, best.m, o);
-        b.i = __shfl_down_sync(0xffffffffu, best.i, o);
-        b.s = __shfl_down_sync(0xffffffffu, best.s, o);
-        best = join(best, b);
+        best.s += __shfl_xor_sync(0xffffffffu, best.s, o);
+        best.i = min(best.i, __shfl_xor_sync(0xffffffffu, best.i, o));
     }
     if (lane == 0) s_best[warp] = best;
     __syncthreads();
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-    if (tid == 0) {
-        for (int w = 1; w < WARPS; ++w) best = join(best, s_best[w]);
-        uint32_t a;
-        asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(&s_cl[rank])));
-        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(best.m) : "memory");
-        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a + 4), "r"(best.i) : "memory");
-        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a + 8), "f"(best.s) : "memory");
+    if (warp == 0) {
+        best = join_lanes(s_best[lane & (WARPS - 1)], WARPS);
+        if (lane == 0) {
+            uint32_t a;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(&s_cl[rank])));
+            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(best.m) : "memory");
+            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a + 4), "r"(best.i) : "memory");
+            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a + 8), "f"(best.s) : "memory");
+        }
+        __syncwarp();
     }
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-    if (rank == 0 && tid == 0) {
-        best = s_cl[0];
-        for (uint32_t c = 1; c < ncl; ++c) best = join(best, s_cl[c]);
-        const bool nan = best.s != best.s;
-        if (p.token) p.token[t] = best.m == NEG ? -1 : best.i;
-        if (p.lse) p.lse[t] = nan ? best.s : best.m == NEG ? NEG : best.m + logf(best.s);
-        if (nan && p.status) atomicOr(p.status, STATUS_NAN_LOGIT);
+    if (rank == 0 && warp == 0) {
+        best = lane < (1 << lg) ? s_cl[lane] : Best{NEG, 0x7fffffff, 0.0f};
+        best = join_lanes(best, MAX_CL);
+        if (lane == 0) {
+            const bool nan = best.s != best.s;
+            if (p.token) p.token[t] = best.m == NEG ? -1 : best.i;
+            if (p.lse) p.lse[t] = nan ? best.s : best.m == NEG ? NEG : best.m + logf(best.s);
+            if (nan && p.status) atomicOr(p.status, STATUS_NAN_LOGIT);
+        }
     }
+}
+
+// Allow clusters of 16 for `kernel` on the current device, once per device
+// (an attribute call that does not have to be made while a stream is captured).
+cudaError_t allow_wide_clusters(const void* kernel) {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (done.load() & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) done.fetch_or(bit);
+    return e;
 }
 
 }  // namespace
@@ -280,15 +452,19 @@ cudaError_t launch_logits(const LogitArgs& p, const DeviceInfo& dev, cudaStream_
     // the wider slice still fits one step.
     int ncl = MAX_CL;
     while (ncl > 1 && ((int64_t)(ncl / 2) * 1024 >= p.V ||
-                       (p.T * (ncl / 2) >= 4 * dev.sm_count && (int64_t)(ncl / 2) * STEP >= p.V)))
+                       (p.T * (ncl / 2) >= 8 * dev.sm_count && (int64_t)(ncl / 2) * STEP >= p.V)))
         ncl /= 2;
     int64_t slice = ceil_div(ceil_div(p.V, ncl), 32) * 32;
     if (slice > MAX_SLICE) slice = MAX_SLICE;
-    const bool dense = p.row_start || p.bias_start;
-    const size_t smem = dense ? 4 * (size_t)slice + (size_t)slice / 8 : 0;
+    const bool sparse = p.row_start || p.bias_start;
+    const size_t smem = (p.mask ? ((size_t)slice / 32 + 3) / 4 * 16 : 0) + (sparse ? 4 * (size_t)slice + (size_t)slice / 4 + 2 * (size_t)slice : 0);
     int per_sm = 0;
     cudaError_t e = kernel_occupancy(reinterpret_cast<const void*>(logits_kernel), THREADS, smem, &per_sm);
     if (e != cudaSuccess) return e;
+    if (ncl > 8) {
+        e = allow_wide_clusters(reinterpret_cast<const void*>(logits_kernel));
+        if (e != cudaSuccess) return e;
+    }
     const int64_t grid = p.T * ncl;
     if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     cudaLaunchAttribute attr;
@@ -302,7 +478,9 @@ cudaError_t launch_logits(const LogitArgs& p, const DeviceInfo& dev, cudaStream_
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, logits_kernel, p, (int)slice);
+    int lg = 0;
+    while ((1 << lg) < ncl) ++lg;
+    return cudaLaunchKernelEx(&cfg, logits_kernel, p, (int)slice, lg);
 }
 
 }  // namespace moeq4
