@@ -396,26 +396,36 @@ def moe_q4_gemv(W: torch.Tensor, x: torch.Tensor, y=None, workspace=None, stream
 
 # ---------------------------------------------------------------- per-request operators around the projections
 
-def _rows(t: torch.Tensor, name: str, device, cols=None, rows=None) -> int:
-    """The row pitch of a 2D fp32 tensor on `device` with contiguous rows."""
-    if t.dtype != torch.float32 or t.dim() != 2 or t.device != device:
-        raise ValueError(f"{name} must be a 2D float32 tensor on {device}")
-    if (cols is not None and t.shape[1] != cols) or (rows is not None and t.shape[0] != rows):
-        raise ValueError(f"{name} is {tuple(t.shape)}, expected ({rows}, {cols})")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+def _rows(t: torch.Tensor, name: str, device: int, rows: int, cols: int) -> int:
+    """The row pitch of a [rows, cols] fp32 tensor on a GPU with contiguous rows."""
+    if t.dtype is not torch.float32 or t.get_device() != device or t.shape != (rows, cols):
+        raise ValueError(f"{name} must be a ({rows}, {cols}) float32 tensor on GPU {device}, "
+                         f"got {tuple(t.shape)} {t.dtype} on {t.device}")
+    pitch, step = t.stride()
+    if step != 1 and cols > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    return pitch if rows > 1 else max(pitch, cols)
 
 
-def _vector(t, name: str, device, dtype, n=None):
-    """The address of a contiguous 1D tensor of n elements, or None."""
+def _vector(t, name: str, device: int, dtype, n=None):
+    """The address of a contiguous 1D tensor (of n elements) on a GPU, or None."""
     if t is None:
         return None
-    if t.dtype != dtype or t.dim() != 1 or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous 1D {dtype} tensor on {device}")
+    if t.dtype is not dtype or t.get_device() != device or t.dim() != 1 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous 1D {dtype} tensor on GPU {device}")
     if n is not None and t.shape[0] != n:
         raise ValueError(f"{name} has {t.shape[0]} elements, expected {n}")
     return t.data_ptr()
+
+
+def _call(f, what: str, device: int, stream, *args):
+    """f(*args, stream) with `device` current; stream None: its current one."""
+    if torch.cuda.current_device() != device:
+        with torch.cuda.device(device):
+            return _call(f, what, device, stream, *args)
+    rc = f(*args, torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream)
+    if rc != MOE_Q4_OK:
+        raise MoeQ4Error(rc, what)
 
 
 class Adapters:
@@ -434,7 +444,7 @@ class Adapters:
             raise ValueError("a and b must be float32, float16 or bfloat16, alike, on one device")
         if not a.is_cuda or not a.is_contiguous() or not b.is_contiguous():
             raise ValueError("a and b must be contiguous, on a GPU")
-        self.a, self.b, self.scale, self.device = a, b, scale, a.device
+        self.a, self.b, self.scale, self.device = a, b, scale, a.get_device()
         self.n_adapters, self.rank, self.hidden = a.shape
         self.n_out = b.shape[1]
         self.struct = _Adapters(self.hidden, self.rank, self.n_out, self.n_adapters, self._DTYPES[a.dtype],
@@ -456,17 +466,19 @@ def moe_q4_adapters_apply(adapters: Adapters, x: torch.Tensor, adapter: torch.Te
     -1: y[t] = base[t]).  base None: zeros; y may be base (in place).  x, base
     and y may be column slices of wider buffers (contiguous rows)."""
     dev = adapters.device
-    T = x.shape[0]
-    ldx = _rows(x, "x", dev, adapters.hidden)
+    T, N = x.shape[0], adapters.n_out
+    ldx = _rows(x, "x", dev, T, adapters.hidden)
     ids = _vector(adapter, "adapter", dev, torch.int32, T)
-    y = torch.empty((T, adapters.n_out), dtype=torch.float32, device=dev) if y is None else y
-    ldy = _rows(y, "y", dev, adapters.n_out, T)
-    ldb = 0 if base is None else _rows(base, "base", dev, adapters.n_out, T)
+    if y is None:
+        y = torch.empty((T, N), dtype=torch.float32, device=x.device)
+    ldy = _rows(y, "y", dev, T, N)
+    pbase, ldb = (None, 0) if base is None else (base.data_ptr(), _rows(base, "base", dev, T, N))
     if workspace is None:
-        workspace = alloc_workspace(moe_q4_adapters_workspace_bytes(adapters, T), dev)
-    with torch.cuda.device(dev):
-        _check(_lib.moe_q4_adapters_apply(adapters.ref, _p(x), ldx, ids, T, _p(base), ldb, _p(y), ldy, _p(workspace),
-                                          workspace.numel(), _stream(stream)), "moe_q4_adapters_apply")
+        workspace = alloc_workspace(moe_q4_adapters_workspace_bytes(adapters, T), x.device)
+    elif workspace.get_device() != dev or workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on GPU {dev}")
+    _call(_lib.moe_q4_adapters_apply, "moe_q4_adapters_apply", dev, stream, adapters.ref, x.data_ptr(), ldx, ids, T,
+          pbase, ldb, y.data_ptr(), ldy, workspace.data_ptr(), workspace.numel())
     return y
 
 
@@ -490,17 +502,17 @@ class LogitRules:
                             repetition=repetition, presence=presence, frequency=frequency, bias_token=bias_token,
                             bias_value=bias_value, bias_start=bias_start, mask=mask, mask_row=mask_row)
 
-    def struct(self, T: int, V: int, device) -> _LogitRules:
-        """The C descriptor for T rows of V logits."""
+    def struct(self, T: int, V: int, device: int) -> _LogitRules:
+        """The C descriptor for T rows of V logits on a GPU."""
         t = self.tensors
         i32, i64, f32 = torch.int32, torch.int64, torch.float32
 
         def ptr(name, dtype, n=None):
             return _vector(t[name], name, device, dtype, n)
         mask = t["mask"]
-        if mask is not None and (mask.dtype != i32 or mask.dim() != 2 or mask.shape[1] != (V + 31) // 32 or
-                                 mask.device != device or not mask.is_contiguous()):
-            raise ValueError(f"mask must be a contiguous [n_masks, {(V + 31) // 32}] int32 tensor on {device}")
+        if mask is not None and (mask.dtype is not i32 or mask.dim() != 2 or mask.shape[1] != (V + 31) // 32 or
+                                 mask.get_device() != device or not mask.is_contiguous()):
+            raise ValueError(f"mask must be a contiguous [n_masks, {(V + 31) // 32}] int32 tensor on GPU {device}")
         n_bias = 0 if t["bias_token"] is None else t["bias_token"].shape[0]
         return _LogitRules(
             V, ptr("tokens", i32), 0 if t["tokens"] is None else t["tokens"].shape[0], ptr("row_start", i64, T + 1),
@@ -519,18 +531,14 @@ def moe_q4_logits_apply(rules: LogitRules, logits: torch.Tensor, out=None, token
     if not logits.is_cuda or logits.dim() != 2:
         raise ValueError("logits must be a 2D tensor on a GPU")
     T, V = logits.shape
-    dev = logits.device
-    ld = _rows(logits, "logits", dev)
+    dev = logits.get_device()
+    ld = _rows(logits, "logits", dev, T, V)
     if out is None and token is None and lse is None:
-        out = torch.empty((T, V), dtype=torch.float32, device=dev)
-    ldo = 0 if out is None else _rows(out, "out", dev, V, T)
-    r = rules.struct(T, V, dev)
-    with torch.cuda.device(dev):
-        _check(_lib.moe_q4_logits_apply(ctypes.byref(r), _p(logits), ld, T, _p(out), ldo,
-                                        _vector(token, "token", dev, torch.int32, T),
-                                        _vector(lse, "lse", dev, torch.float32, T),
-                                        _vector(status, "status", dev, torch.int32, 1), _stream(stream)),
-               "moe_q4_logits_apply")
+        out = torch.empty((T, V), dtype=torch.float32, device=logits.device)
+    pout, ldo = (None, 0) if out is None else (out.data_ptr(), _rows(out, "out", dev, T, V))
+    _call(_lib.moe_q4_logits_apply, "moe_q4_logits_apply", dev, stream, ctypes.byref(rules.struct(T, V, dev)),
+          logits.data_ptr(), ld, T, pout, ldo, _vector(token, "token", dev, torch.int32, T),
+          _vector(lse, "lse", dev, torch.float32, T), _vector(status, "status", dev, torch.int32, 1))
     return out, token, lse
 
 
