@@ -17,6 +17,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "common.cuh"
@@ -37,7 +38,6 @@ constexpr int GROUP_THREADS = 1024;
 constexpr int GROUP_IDS = 16;     // ids per thread of the grouping kernels
 constexpr int GROUP_CHUNK = GROUP_THREADS * GROUP_IDS;
 constexpr int MAX_ADAPTERS = 1024;
-constexpr int TILE_MIN_ROWS = 16; // rows per adapter from which the tile kernel is used
 
 // ------------------------------------------------------------------ clusters
 
@@ -218,7 +218,7 @@ __device__ __forceinline__ void expand_columns(const W* b, const AdapterArgs& p,
 // cluster barrier every CTA has u and produces its own columns, a column per
 // thread.  A is thus read once per chunk (from L2 after the first time).
 template <class W, bool INLINE>
-__global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(THREADS)
+__global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(THREADS, 4)
     adapters_rows_kernel(const __grid_constant__ AdapterArgs p, int chunks, int iters) {
     __shared__ int s_ids[INLINE_T];
     __shared__ int s_starts[2];
@@ -1166,10 +1166,11 @@ template <class W>
 cudaError_t launch_rows(const AdapterArgs& p, const DeviceInfo& dev, cudaStream_t s) {
     const bool in = p.T <= INLINE_T;
     const int64_t groups = in ? std::min<int64_t>(p.T, (p.n + 1) + p.T / ROWS) : p.T / ROWS + p.n + 1;
-    // columns per cluster: as many steps of COLS as leave two clusters' worth
-    // of CTAs for every 8 SMs; u is computed once per cluster
+    // columns per cluster: as many steps of COLS as leave four CTAs an SM; u is
+    // computed once per cluster (8 adapters, rank 16, on 131072 columns: two
+    // CTAs an SM 23.6 us, four 16.3, eight 18.0)
     const int64_t steps = ceil_div(p.N, COLS);
-    const int64_t iters = std::max<int64_t>(1, std::min<int64_t>(steps, groups * steps / (2 * dev.sm_count / CL)));
+    const int64_t iters = std::max<int64_t>(1, std::min<int64_t>(steps, groups * steps / (4 * dev.sm_count / CL)));
     const int64_t chunks = ceil_div(steps, iters);
     const int64_t grid = groups * chunks * CL;
     if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
@@ -1195,27 +1196,43 @@ cudaError_t launch_tiles(const AdapterArgs& p, cudaStream_t s) {
     return launch_clusters(adapters_tile_kernel<W, CLT>, (unsigned)(tiles * CLT), CLT, TT, smem, true, s, p);
 }
 
-// The choice of kernel.  Tiles pay off once adapters see enough rows to fill
-// a good part of one.  CLT: the tile kernel has one CTA an SM, so the widest
-// cluster that still runs all tiles at once (about 12 of 13 SMs can hold
-// clusters of 4, and 15 clusters of 8 fit); but wide enough that an
-// accumulator of step 1 sums no more than CHAIN panels, since each addition
-// truncates (4 CHAIN additions drift by about 1e-6 of the sum).
+// The choice of kernel and of the tile kernel's cluster, by what the steps of
+// either were measured to take (us; H = 256 .. 2048, N = 300 .. 16384):
+//   rows: 9 + 3e-6 * tiles of 8 rows * r (H + N);
+//   tiles: 5 + waves * (4 + 0.6 a panel of H + 2 a block of y, per CTA), one CTA
+//   an SM (about 12 of 13 SMs can hold clusters of 4, and 15 clusters of 8 fit).
+// (2048 -> 2048, rank 16, 4 adapters: 256 rows 13.9 us as rows, 17.9 as tiles;
+// 512 rows 23.9 and 18.7.  Rank 64: 128 rows 27.7 and 21.0.)  A cluster must be
+// wide enough that an accumulator of step 1 sums no more than CHAIN panels:
+// each addition truncates, and 4 CHAIN of them drift by about 1e-6 of the sum.
 template <class W>
 cudaError_t launch_typed(const AdapterArgs& p, const DeviceInfo& dev, cudaStream_t s) {
     constexpr int CHAIN = 10;
+    if (p.T <= INLINE_T) return launch_rows<W>(p, dev, s);
     const int n16 = (p.r + 15) / 16 * 16, accs = std::min(MAX_ACCS, (int)COLS_TMEM / n16 - 1), chunks = p.H / PK;
-    if (getenv("ROWS")) return launch_rows<W>(p, dev, s);
-    if (p.T <= INLINE_T || p.T < (int64_t)TILE_MIN_ROWS * p.n || chunks > CL * accs * CHAIN) return launch_rows<W>(p, dev, s);
-    // adapters with a tile each while they see fewer rows than a tile has, else half a tile too many each
-    const int64_t tiles = p.T < (int64_t)TM * (p.n + 1) ? std::min<int64_t>(p.T, p.n + 1) : p.T / TM + (p.n + 1) / 2;
-    const auto fits = [&](int c) { return tiles * c <= (c <= 2 ? dev.sm_count : c == 4 ? dev.sm_count * 12 / 13 : 15 * dev.sm_count / 148 * 8); };
-    const auto short_enough = [&](int c) { return chunks <= c * accs * CHAIN; };
-    { const char* e = getenv("CLT"); const int c = e ? atoi(e) : 0; if (c) return c == 1 ? launch_tiles<W, 1>(p, s) : c == 2 ? launch_tiles<W, 2>(p, s) : c == 4 ? launch_tiles<W, 4>(p, s) : launch_tiles<W, 8>(p, s); }
-    if (fits(8) || !short_enough(4)) return launch_tiles<W, 8>(p, s);
-    if (fits(4) || !short_enough(2)) return launch_tiles<W, 4>(p, s);
-    if (fits(2) || !short_enough(1)) return launch_tiles<W, 2>(p, s);
-    return launch_tiles<W, 1>(p, s);
+    // tiles of `rows` rows: one an adapter while adapters see fewer, else half a tile too many each
+    const auto tiles = [&](int rows) {
+        return (double)(p.T < (int64_t)rows * (p.n + 1) ? std::min<int64_t>(p.T, p.n + 1) : p.T / rows + (p.n + 1) / 2);
+    };
+    double best = 9.0 + 3e-6 * std::min<double>((double)p.T, (double)(p.T / ROWS + (p.n + 1) / 2)) * p.r * (double)(p.H + p.N);
+    int cl = 0;
+    for (int c = 1; c <= CL; c *= 2) {
+        if (chunks > c * accs * CHAIN) continue;
+        const int slots = c <= 2 ? dev.sm_count : c == 4 ? dev.sm_count * 12 / 13 : 15 * CL * dev.sm_count / 148;
+        const double t = 5.0 + std::ceil(tiles(TM) * c / slots) *
+                                   (4.0 + 0.6 * chunks / c + 2.0 * (double)ceil_div(ceil_div(p.N, TM), c));
+        if (t < best) {
+            best = t;
+            cl = c;
+        }
+    }
+    switch (cl) {
+        case 1: return launch_tiles<W, 1>(p, s);
+        case 2: return launch_tiles<W, 2>(p, s);
+        case 4: return launch_tiles<W, 4>(p, s);
+        case 8: return launch_tiles<W, 8>(p, s);
+        default: return launch_rows<W>(p, dev, s);
+    }
 }
 
 }  // namespace
