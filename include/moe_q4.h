@@ -347,7 +347,8 @@ int moe_q4_adapters_apply(const moe_q4_adapters* A, const float* x, int64_t ldx,
  * status (device uint32, may be NULL): MOE_Q4_STATUS_BAD_MASK_INDEX and, when
  * token or lse is asked for, MOE_Q4_STATUS_NAN_LOGIT are OR-ed into it.
  * 1 <= vocab <= 2^30, pitches >= vocab; T <= 2^24; all arrays 4-byte
- * aligned, the start arrays 8-byte, tokens 16-byte.  No workspace, no host
+ * aligned, the start arrays 8-byte, tokens 16-byte; no output may overlap
+ * another one or an input (but for out in place).  No workspace, no host
  * synchronisation; capturable.
  * --------------------------------------------------------------------- */
 typedef struct {

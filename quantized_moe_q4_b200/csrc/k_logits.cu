@@ -11,11 +11,12 @@
 // would all fall to one CTA if each owned a range).  While the logits are on
 // their way to L2, the few that penalties and biases change are worked out in
 // shared memory: a 32-bit word per token counts its occurrences in the row's
-// history, a list keeps the tokens that occur, their ruled logits replace
-// their counts, and a bit per token says where that was done.  Then the logits
-// are streamed once: four of them cost one test of four bits, the mask, a
-// running maximum and, relative to the warp's maximum, one exponential each.
-// The CTAs' (maximum, lowest token, sum) are joined through distributed shared
+// history and a bit says that there is one (two shared atomics a token, nothing
+// that waits for them, so that long histories scan fast), the set bits become a
+// list, and all threads fetch and rule the logits on it.  Then the logits are
+// streamed once: four of them cost one test of four bits, the mask, a running
+// maximum and, relative to the warp's maximum, one exponential each.  The
+// CTAs' (maximum, lowest token, sum) are joined through distributed shared
 // memory.  Bound by the logits' bytes (read, and written if asked for); CTAs
 // are small, so that four of them an SM cover one another's latencies.
 #include <algorithm>
@@ -36,7 +37,7 @@ constexpr int MAX_CL = 16;          // CTAs per cluster (beyond 8: not portable,
 constexpr int BATCH = 8;            // 16-byte accesses in flight per thread
 constexpr int STEP = THREADS * 4 * BATCH;  // logits a CTA holds at a time
 constexpr int FIRST_CTAS = 592;     // CTAs that ask for the lists of all rows (about the first to run)
-constexpr int MAX_SLICE = 4 * STEP;  // logits whose words and list fit the shared memory (200 KB)
+constexpr int MAX_SLICE = 4 * STEP;  // logits whose words fit the shared memory (128 KB)
 
 // History word of a token: bit 31: it occurs in the prompt; low bits: times generated.
 constexpr uint32_t IN_PROMPT = 0x80000000u;
@@ -127,7 +128,7 @@ __device__ __forceinline__ void each_token(const int32_t* list, int64_t lo, int6
 // with histories or biases words[slice] (history word, or for a ruled token
 // the bits of its logit), ruled[slice / 32] (bit set: the word is such a
 // logit), listed[slice / 32] (bit set: a bias lists the token), seen[slice]
-// (16-bit: the tokens of the history, once each).  Place i of a CTA's `slice`
+// (16-bit: the places of the history's tokens).  Place i of a CTA's `slice`
 // (a multiple of 32) is token base + 32 * (i / 32 * ncl + rank) + i % 32, with
 // ncl = 1 << lg CTAs in the cluster.
 __global__ void __launch_bounds__(THREADS, 4) logits_kernel(const __grid_constant__ LogitArgs p, int slice, int lg) {
@@ -233,27 +234,55 @@ __global__ void __launch_bounds__(THREADS, 4) logits_kernel(const __grid_constan
                 each_token(p.tokens, h0, h1, [&](int v, int64_t at) {
                     uint32_t i;
                     if (!inside(v, i)) return;
-                    const uint32_t bit = 1u << (i & 31);
                     if (at >= hg) atomicAdd(&words[i], 1u);
-                    else if (!(words[i] & IN_PROMPT)) atomicOr(&words[i], IN_PROMPT);
-                    if (!(ruled[i >> 5] & bit) && !(atomicOr(&ruled[i >> 5], bit) & bit)) seen[atomicAdd(&s_seen, 1)] = (uint16_t)i;
+                    else atomicOr(&words[i], IN_PROMPT);
+                    atomicOr(&ruled[i >> 5], 1u << (i & 31));
                 });
+                // (a thread's first bias entry stays in registers, its logit on the way)
+                uint32_t bias_at = ~0u;
+                float bias_logit = 0.0f, bias_add = 0.0f;
                 for (int64_t e = b0 + tid; e < b1; e += THREADS) {
                     uint32_t i;
                     if (!inside(__ldg(p.bias_token + e), i)) continue;
                     const uint32_t bit = 1u << (i & 31);
                     if (atomicOr(&listed[i >> 5], bit) & bit) s_dup = 1;
+                    if (e == b0 + tid) {
+                        bias_at = i;
+                        bias_logit = src[token_at(i)];
+                        bias_add = __ldg(p.bias_value + e);
+                    }
                 }
                 __syncthreads();
-                const int n = s_seen;
-#pragma unroll 4
-                for (int e = tid; e < n; e += THREADS) {
-                    const int i = seen[e];
-                    words[i] = __float_as_uint(penalise(src[token_at(i)], words[i], row));
+                // the places whose bits are set, as a list; their logits are fetched
+                // and ruled by all threads alike
+                if (h1 > h0) {
+                    for (int g0 = 0; g0 < len / 32; g0 += THREADS) {
+                        uint32_t bits = g0 + tid < len / 32 ? ruled[g0 + tid] : 0u;
+                        const int mine = __popc(bits);
+                        int before = mine;
+#pragma unroll
+                        for (int o = 1; o < 32; o <<= 1) {
+                            const int q = __shfl_up_sync(0xffffffffu, before, o);
+                            if (lane >= o) before += q;
+                        }
+                        int at = 0;
+                        if (lane == 31 && before) at = atomicAdd(&s_seen, before);
+                        at = __shfl_sync(0xffffffffu, at, 31) + before - mine;
+                        for (; bits; bits &= bits - 1) seen[at++] = (uint16_t)(32 * (g0 + tid) + __ffs(bits) - 1);
+                    }
+                    __syncthreads();
+                    const int n = s_seen;
+#pragma unroll 2
+                    for (int e = tid; e < n; e += THREADS) {
+                        const int i = seen[e];
+                        words[i] = __float_as_uint(penalise(src[token_at(i)], words[i], row));
+                    }
                 }
                 if (b1 > b0) {
                     __syncthreads();
                     for (int64_t e = b0 + tid; e < b1; e += THREADS) {
+                        const bool kept = e == b0 + tid;
+                        if (kept && bias_at == ~0u) continue;
                         const int v = __ldg(p.bias_token + e);
                         uint32_t i;
                         if (!inside(v, i)) continue;
@@ -262,8 +291,9 @@ __global__ void __launch_bounds__(THREADS, 4) logits_kernel(const __grid_constan
                             for (int64_t f = e + 1; f < b1 && last; ++f) last = __ldg(p.bias_token + f) != v;
                         if (!last) continue;
                         const uint32_t bit = 1u << (i & 31);
-                        const float l = atomicOr(&ruled[i >> 5], bit) & bit ? __uint_as_float(words[i]) : src[token_at(i)];
-                        words[i] = __float_as_uint(__fadd_rn(l, __ldg(p.bias_value + e)));
+                        const bool set = atomicOr(&ruled[i >> 5], bit) & bit;
+                        const float l = set ? __uint_as_float(words[i]) : kept ? bias_logit : src[token_at(i)];
+                        words[i] = __float_as_uint(__fadd_rn(l, kept ? bias_add : __ldg(p.bias_value + e)));
                     }
                 }
             }
