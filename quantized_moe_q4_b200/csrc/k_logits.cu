@@ -17,10 +17,10 @@
 // streamed once: four of them cost one test of four bits, the mask, a running
 // maximum and, relative to the warp's maximum, one exponential each.  The
 // CTAs' (maximum, lowest token, sum) are joined through distributed shared
-// memory.  Bound by the logits' bytes (read, and written if asked for); CTAs
-// are small, so that four of them an SM cover one another's latencies.
+// memory.  Bound by the logits' bytes (read, and written if asked for) without
+// rules; with them a CTA spends half its time in the chain of dependent loads
+// (row, tokens, their logits), which two CTAs an SM cover in part.
 #include <algorithm>
-#include <atomic>
 #include <type_traits>
 
 #include "common.cuh"
@@ -31,13 +31,12 @@ namespace moeq4 {
 
 namespace {
 
-constexpr int THREADS = 256;
+constexpr int THREADS = 512;
 constexpr int WARPS = THREADS / 32;
-constexpr int MAX_CL = 16;          // CTAs per cluster (beyond 8: not portable, allowed on sm_100a)
+constexpr int MAX_CL = 8;           // CTAs per cluster (the portable limit)
 constexpr int BATCH = 8;            // 16-byte accesses in flight per thread
 constexpr int STEP = THREADS * 4 * BATCH;  // logits a CTA holds at a time
-constexpr int FIRST_CTAS = 592;     // CTAs that ask for the lists of all rows (about the first to run)
-constexpr int MAX_SLICE = 4 * STEP;  // logits whose words fit the shared memory (128 KB)
+constexpr int MAX_SLICE = 2 * STEP;  // logits whose words fit the shared memory (128 KB)
 
 // History word of a token: bit 31: it occurs in the prompt; low bits: times generated.
 constexpr uint32_t IN_PROMPT = 0x80000000u;
@@ -131,7 +130,7 @@ __device__ __forceinline__ void each_token(const int32_t* list, int64_t lo, int6
 // (16-bit: the places of the history's tokens).  Place i of a CTA's `slice`
 // (a multiple of 32) is token base + 32 * (i / 32 * ncl + rank) + i % 32, with
 // ncl = 1 << lg CTAs in the cluster.
-__global__ void __launch_bounds__(THREADS, 4) logits_kernel(const __grid_constant__ LogitArgs p, int slice, int lg) {
+__global__ void __launch_bounds__(THREADS, 2) logits_kernel(const __grid_constant__ LogitArgs p, int slice, int lg) {
     extern __shared__ __align__(16) uint32_t s_mem[];
     __shared__ Best s_best[WARPS];
     __shared__ Best s_cl[MAX_CL];
@@ -151,31 +150,13 @@ __global__ void __launch_bounds__(THREADS, 4) logits_kernel(const __grid_constan
     float* out = p.out ? p.out + t * p.ldo : nullptr;
     const auto token_at = [&](uint32_t i) { return (((i >> 5 << lg) + rank) << 5) + (i & 31); };  // less base
 
-    // What the rules need comes through a chain of dependent loads, which a
-    // busy memory makes long: the logits are asked for before it begins, and
-    // the lists of all rows by the first CTAs, a share each.
-    const bool ruling = p.row_start || p.bias_start || p.mask;
-    if (ruling) {
+    // What the rules need comes through a chain of dependent loads: the logits
+    // are asked for before it begins.
+    if (p.row_start || p.bias_start || p.mask)
         for (int g = tid; g < slice / 32; g += THREADS) {
             const uint32_t v = token_at(32 * g);
             if (v < p.V) prefetch_l2(in + v);
         }
-        if (blockIdx.x < FIRST_CTAS) {
-            const int64_t c = (int64_t)blockIdx.x * THREADS + tid, all = (int64_t)min(gridDim.x, (unsigned)FIRST_CTAS) * THREADS;
-            if (p.row_start) {
-                for (int64_t i = 32 * c; i < p.n_tokens; i += 32 * all) prefetch_l2(p.tokens + i);
-                for (int64_t i = 16 * c; i < p.T; i += 16 * all) {
-                    prefetch_l2(p.row_start + i);
-                    if (p.generated) prefetch_l2(p.generated + i);
-                }
-            }
-            if (p.bias_start)
-                for (int64_t i = 32 * c; i < p.n_bias; i += 32 * all) {
-                    prefetch_l2(p.bias_token + i);
-                    prefetch_l2(p.bias_value + i);
-                }
-        }
-    }
 
     int64_t h0 = 0, h1 = 0, hg = 0, b0 = 0, b1 = 0;
     if (p.row_start) {
@@ -218,7 +199,7 @@ __global__ void __launch_bounds__(THREADS, 4) logits_kernel(const __grid_constan
                 i = (g >> lg << 5) + (u & 31);
                 return u < (uint32_t)left && (g & ((1u << lg) - 1)) == rank;
             };
-            __syncthreads();  // (an earlier turn's words are done with)
+            if (base) __syncthreads();  // (an earlier turn's words are done with)
             if (mask)
                 for (int g = tid; g < len / 32; g += THREADS) s_mem[g] = __ldg(mask + (base >> 5) + (((uint32_t)g << lg) + rank));
             if (sparse) {
@@ -447,8 +428,9 @@ __global__ void __launch_bounds__(THREADS, 4) logits_kernel(const __grid_constan
         __syncwarp();
     }
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    if (rank != 0) return;  // (nobody reads this CTA's memory)
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-    if (rank == 0 && warp == 0) {
+    if (warp == 0) {
         best = lane < (1 << lg) ? s_cl[lane] : Best{NEG, 0x7fffffff, 0.0f};
         best = join_lanes(best, MAX_CL);
         if (lane == 0) {
@@ -460,29 +442,17 @@ __global__ void __launch_bounds__(THREADS, 4) logits_kernel(const __grid_constan
     }
 }
 
-// Allow clusters of 16 for `kernel` on the current device, once per device
-// (an attribute call that does not have to be made while a stream is captured).
-cudaError_t allow_wide_clusters(const void* kernel) {
-    static std::atomic<uint64_t> done{0};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const uint64_t bit = uint64_t(1) << (dev & 63);
-    if (done.load() & bit) return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e == cudaSuccess) done.fetch_or(bit);
-    return e;
-}
-
 }  // namespace
 
 cudaError_t launch_logits(const LogitArgs& p, const DeviceInfo& dev, cudaStream_t s) {
-    // As many CTAs a row as the portable cluster has, fewer where a slice
-    // would be under a thousand logits, or where rows alone fill the GPU and
-    // the wider slice still fits one step.
+    // 8 CTAs a row; fewer where a slice would be under a thousand logits, or
+    // where rows alone fill the GPU and the wider slice still fits one step.
+    // (16 CTAs of 256 threads a row: 8.2 us for one row of 131072 instead of 9.3,
+    // but 39 for 64 rows with histories instead of 34, and 30 for 32 rows of
+    // 16384 tokens each instead of 23.)
     int ncl = MAX_CL;
     while (ncl > 1 && ((int64_t)(ncl / 2) * 1024 >= p.V ||
-                       (p.T * (ncl / 2) >= 8 * dev.sm_count && (int64_t)(ncl / 2) * STEP >= p.V)))
+                       (p.T * (ncl / 2) >= 4 * dev.sm_count && (int64_t)(ncl / 2) * STEP >= p.V)))
         ncl /= 2;
     int64_t slice = ceil_div(ceil_div(p.V, ncl), 32) * 32;
     if (slice > MAX_SLICE) slice = MAX_SLICE;
@@ -491,10 +461,6 @@ cudaError_t launch_logits(const LogitArgs& p, const DeviceInfo& dev, cudaStream_
     int per_sm = 0;
     cudaError_t e = kernel_occupancy(reinterpret_cast<const void*>(logits_kernel), THREADS, smem, &per_sm);
     if (e != cudaSuccess) return e;
-    if (ncl > 8) {
-        e = allow_wide_clusters(reinterpret_cast<const void*>(logits_kernel));
-        if (e != cudaSuccess) return e;
-    }
     const int64_t grid = p.T * ncl;
     if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     cudaLaunchAttribute attr;
