@@ -55,10 +55,6 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t smem_addr, uint32_t rank) 
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr), "r"(rank));
     return a;
 }
-__device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-}
-
 __device__ __forceinline__ void st_cluster4(uint32_t addr, float4 v) {
     asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
                  : "memory");
@@ -106,67 +102,79 @@ __device__ __forceinline__ void load8(const W* p, float (&v)[8]) {
     unpack8(__ldg(reinterpret_cast<const uint4*>(p)), v, p);
 }
 
+// The same in two steps, so that several loads can be in flight.
+template <class W>
+struct Raw8 {
+    uint4 q;
+    __device__ __forceinline__ void load(const W* p) { q = __ldg(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void unpack(float (&v)[8]) const { unpack8(q, v, (const W*)nullptr); }
+};
+template <>
+struct Raw8<float> {
+    float v_[8];
+    __device__ __forceinline__ void load(const float* p) { load8(p, v_); }
+    __device__ __forceinline__ void unpack(float (&v)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = v_[i];
+    }
+};
+
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // ------------------------------------------------------------------ rows kernel
 
-// Where a CTA's shrink work lies: the cluster's 8 CTAs split the r rows of A
-// into blocks of 8 rows (a row per warp) and, where fewer than 8 blocks
-// exist, H into `splits` interleaved parts.
-struct ShrinkPart {
-    int splits;
-    __device__ explicit ShrinkPart(int r) : splits(r > 32 ? 1 : CL / (r / 8)) {}
-};
-
-// u[row] of NT rows of x with one row of A (this warp's), over the 256-wide
-// pieces `piece`, piece + step, ... of H; the sums of all lanes go to every
-// CTA's part[][row][k].
+// u of NT rows of x, this CTA's share: H comes in pieces of 256 columns, piece p
+// the work of CTA p % CL; with fewer pieces than CTAs, `sharing` CTAs take the
+// rows of A of one piece in turn, eight at a time.  A lane keeps its eight
+// columns of the NT rows in registers over all rows of A; a warp's row of A is
+// one product, whose sums over the lanes go to part[row][k] of this CTA (added
+// to what is there).  KF rows of A are in flight at a time.
 template <class W, int NT>
-__device__ __forceinline__ void shrink_row(const W* arow, const AdapterArgs& p, const int* tok, int cnt, int piece,
-                                           int step, float* part, int k) {
-    const int lane = threadIdx.x & 31;
-    float acc[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) acc[t] = 0.0f;
-    const float* xr[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) xr[t] = p.x + (int64_t)tok[t < cnt ? t : 0] * p.ldx + 8 * lane;
-#pragma unroll 2
-    for (int h = piece * 256; h < p.H; h += step * 256) {
-        float w[8];
-        load8(arow + h + 8 * lane, w);
+__device__ __forceinline__ void shrink(const W* a, const AdapterArgs& p, const int* tok, int cnt, int rank, float* part) {
+    constexpr int KF = sizeof(W) == 4 ? 2 : 4;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, pieces = p.H / 256;
+    const int sharing = pieces < CL ? CL / pieces : 1, turn = pieces < CL ? rank / pieces : 0;
+    if (turn >= sharing) return;
+    for (int piece = pieces < CL ? rank % pieces : rank; piece < pieces; piece += CL) {
+        float v[NT][8];
 #pragma unroll
         for (int t = 0; t < NT; ++t)
-            if (t < cnt) {
-                float v[8];
-                load8(xr[t] + h, v);
+            if (t < cnt) load8(p.x + (int64_t)tok[t] * p.ldx + piece * 256 + 8 * lane, v[t]);
+        const W* ar = a + piece * 256 + 8 * lane;
+        for (int k0 = turn * 8 + warp; k0 < p.r; k0 += 8 * sharing * KF) {
+            Raw8<W> raw[KF];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) acc[t] = fmaf(w[i], v[i], acc[t]);
+            for (int j = 0; j < KF; ++j) {
+                const int k = k0 + 8 * sharing * j;
+                if (k < p.r) raw[j].load(ar + (int64_t)k * p.H);
             }
-    }
-    const uint32_t dst = smem_u32(part);
-    if constexpr (NT == 1) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], o);
-        if (lane < CL) st_cluster(map_rank(dst + 4u * (uint32_t)k, (uint32_t)lane), acc[0]);
-    } else {
-        // transposing reduction: after it, lane l holds row l / 4's sum
-        static_assert(NT == 8);
+            for (int j = 0; j < KF; ++j) {
+                const int k = k0 + 8 * sharing * j;
+                if (k >= p.r) break;
+                float w[8], acc[NT];
+                raw[j].unpack(w);
 #pragma unroll
-        for (int o = 16, m = 4; m > 0; o >>= 1, m >>= 1)
+                for (int t = 0; t < NT; ++t) {
+                    acc[t] = 0.0f;
+                    if (t < cnt)
 #pragma unroll
-            for (int i = 0; i < m; ++i) {
-                const bool up = (lane & o) != 0;
-                const float keep = up ? acc[i + m] : acc[i], send = up ? acc[i] : acc[i + m];
-                acc[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+                        for (int i = 0; i < 8; ++i) acc[t] = fmaf(w[i], v[t][i], acc[t]);
+                }
+                // transposing reduction: after it, lane l holds the sum of row l * NT / 32
+#pragma unroll
+                for (int o = 16, m = NT / 2; m > 0; o >>= 1, m >>= 1)
+#pragma unroll
+                    for (int i = 0; i < m; ++i) {
+                        const bool up = (lane & o) != 0;
+                        const float keep = up ? acc[i + m] : acc[i], send = up ? acc[i] : acc[i + m];
+                        acc[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+                    }
+#pragma unroll
+                for (int o = 16 / NT; o > 0; o >>= 1) acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], o);
+                const int t = lane / (32 / NT);
+                if (lane % (32 / NT) == 0 && t < cnt) part[t * p.r + k] += acc[0];
             }
-        acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], 2);
-        acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], 1);
-        const int t = lane >> 2;
-        if (t < cnt) {
-            const uint32_t a = dst + 4u * (uint32_t)(t * p.r + k);
-            st_cluster(map_rank(a, (uint32_t)(lane & 3) * 2), acc[0]);
-            st_cluster(map_rank(a, (uint32_t)(lane & 3) * 2 + 1), acc[0]);
         }
     }
 }
@@ -214,9 +222,9 @@ __device__ __forceinline__ void expand_columns(const W* b, const AdapterArgs& p,
 
 // A cluster's work: tile g of up to ROWS rows with one adapter, and columns
 // [chunk * iters * COLS, + iters * COLS) of y.  Each CTA computes its part of
-// u (8 rows of A x a part of H) and stores it to all 8 CTAs; after one
-// cluster barrier every CTA has u and produces its own columns, a column per
-// thread.  A is thus read once per chunk (from L2 after the first time).
+// u; after one cluster barrier every CTA adds all parts, always in the same
+// order, and produces its own columns, a column per thread.  A is thus read
+// once per chunk (from L2 after the first time).
 template <class W, bool INLINE>
 __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(THREADS, 4)
     adapters_rows_kernel(const __grid_constant__ AdapterArgs p, int chunks, int iters) {
@@ -292,35 +300,39 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(THREADS, 4)
         }
         return;
     }
-    cluster_arrive();  // (every CTA of the cluster has started once this completes)
     const W* a = static_cast<const W*>(p.a) + (int64_t)id * p.r * p.H;
     const W* b = static_cast<const W*>(p.b) + (int64_t)id * p.N * p.r;
     // this thread's first rows of B are on their way to L2 while u is computed
     for (int64_t n = n0; n < n1 && n < n0 + 2 * COLS; n += COLS)
         for (int o = 0; o < p.r * (int)sizeof(W); o += 128) prefetch_l2(reinterpret_cast<const char*>(b + n * p.r) + o);
-    const int splits = ShrinkPart(p.r).splits, blocks = p.r / 8;
-    cluster_wait();
-    for (int rb = rank / splits; rb < blocks; rb += CL / splits) {
-        const int k = rb * 8 + warp, piece = rank % splits;
-        float* part = s_part + piece * ROWS * p.r;
-        if (cnt == 1)
-            shrink_row<W, 1>(a + (int64_t)k * p.H, p, s_tok, cnt, piece, splits, part, k);
-        else
-            shrink_row<W, 8>(a + (int64_t)k * p.H, p, s_tok, cnt, piece, splits, part, k);
-    }
+    // (parts of u that nobody computes are zero: fewer pieces than CTAs, shared rows)
+    for (int i = tid; i < cnt * p.r; i += THREADS) s_part[i] = 0.0f;
+    __syncthreads();
+    if (cnt == 1)
+        shrink<W, 1>(a, p, s_tok, cnt, (int)rank, s_part);
+    else
+        for (int t = 0; t < cnt; t += 4) shrink<W, 4>(a, p, s_tok + t, min(4, cnt - t), (int)rank, s_part + t * p.r);
     cluster_arrive();
     cluster_wait();
     const float scale = p.scale ? __ldg(p.scale + id) : 1.0f;
-    for (int i = tid; i < cnt * p.r; i += THREADS) {
-        float v = 0.0f;
-        for (int s = 0; s < splits; ++s) v += s_part[s * ROWS * p.r + i];
-        s_u[i] = v * scale;
+    for (int i = tid; i < cnt * p.r / 4; i += THREADS) {
+        float4 part[CL];
+#pragma unroll
+        for (int c = 0; c < CL; ++c) part[c] = ld_cluster4(map_rank(smem_u32(s_part + 4 * i), (uint32_t)c));
+        float4 v = part[0];
+#pragma unroll
+        for (int c = 1; c < CL; ++c) {
+            v.x += part[c].x; v.y += part[c].y; v.z += part[c].z; v.w += part[c].w;
+        }
+        reinterpret_cast<float4*>(s_u)[i] = make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale);
     }
+    cluster_arrive();  // (this CTA has read the others' parts)
     __syncthreads();
     if (cnt == 1)
         expand_columns<W, 1>(b, p, s_tok, cnt, s_u, n0, n1);
     else
         expand_columns<W, 8>(b, p, s_tok, cnt, s_u, n0, n1);
+    cluster_wait();  // (the others have read this CTA's part)
 }
 
 // ------------------------------------------------------------------ tile kernel

@@ -445,15 +445,23 @@ __global__ void __launch_bounds__(THREADS, 2) logits_kernel(const __grid_constan
 }  // namespace
 
 cudaError_t launch_logits(const LogitArgs& p, const DeviceInfo& dev, cudaStream_t s) {
-    // 8 CTAs a row; fewer where a slice would be under a thousand logits, or
-    // where rows alone fill the GPU and the wider slice still fits one step.
-    // (16 CTAs of 256 threads a row: 8.2 us for one row of 131072 instead of 9.3,
-    // but 39 for 64 rows with histories instead of 34, and 30 for 32 rows of
-    // 16384 tokens each instead of 23.)
-    int ncl = MAX_CL;
-    while (ncl > 1 && ((int64_t)(ncl / 2) * 1024 >= p.V ||
-                       (p.T * (ncl / 2) >= 4 * dev.sm_count && (int64_t)(ncl / 2) * STEP >= p.V)))
-        ncl /= 2;
+    // CTAs a row, two an SM at a time: a CTA takes about 6 us for the rules (3
+    // without) and 3 us for STEP logits, so as many as make the fewest turns,
+    // each with at most STEP logits where 8 CTAs allow that.  (16 CTAs of 256
+    // threads a row: 8.2 us for one row of 131072 instead of 9.3, but 39 for 64
+    // rows with histories instead of 34, and 30 for 32 rows of 16384 tokens each
+    // instead of 23.)
+    int ncl = 1;
+    double best = 0.0;
+    for (int c = 1; c <= MAX_CL; c *= 2) {
+        const int64_t part = ceil_div(p.V, c);
+        if (part > STEP && c < MAX_CL) continue;
+        const double us = (double)ceil_div(p.T * c, 2 * dev.sm_count) * ((p.row_start || p.bias_start ? 6.0 : 3.0) + 3.0 * part / STEP);
+        if (best == 0.0 || us < best) {
+            best = us;
+            ncl = c;
+        }
+    }
     int64_t slice = ceil_div(ceil_div(p.V, ncl), 32) * 32;
     if (slice > MAX_SLICE) slice = MAX_SLICE;
     const bool sparse = p.row_start || p.bias_start;
