@@ -138,43 +138,42 @@ __device__ __forceinline__ void shrink(const W* a, const AdapterArgs& p, const i
     for (int piece = pieces < CL ? rank % pieces : rank; piece < pieces; piece += CL) {
         float v[NT][8];
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int t = 0; t < NT; ++t) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[t][i] = 0.0f;
             if (t < cnt) load8(p.x + (int64_t)tok[t] * p.ldx + piece * 256 + 8 * lane, v[t]);
+        }
         const W* ar = a + piece * 256 + 8 * lane;
         for (int k0 = turn * 8 + warp; k0 < p.r; k0 += 8 * sharing * KF) {
             Raw8<W> raw[KF];
 #pragma unroll
-            for (int j = 0; j < KF; ++j) {
-                const int k = k0 + 8 * sharing * j;
-                if (k < p.r) raw[j].load(ar + (int64_t)k * p.H);
-            }
+            for (int j = 0; j < KF; ++j) raw[j].load(ar + (int64_t)min(k0 + 8 * sharing * j, p.r - 1) * p.H);
+            float acc[KF * NT];  // row t, k0 + 8 sharing j at NT j + t
 #pragma unroll
             for (int j = 0; j < KF; ++j) {
-                const int k = k0 + 8 * sharing * j;
-                if (k >= p.r) break;
-                float w[8], acc[NT];
+                float w[8];
                 raw[j].unpack(w);
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
-                    acc[t] = 0.0f;
-                    if (t < cnt)
+                    acc[NT * j + t] = 0.0f;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) acc[t] = fmaf(w[i], v[t][i], acc[t]);
+                    for (int i = 0; i < 8; ++i) acc[NT * j + t] = fmaf(w[i], v[t][i], acc[NT * j + t]);
                 }
-                // transposing reduction: after it, lane l holds the sum of row l * NT / 32
-#pragma unroll
-                for (int o = 16, m = NT / 2; m > 0; o >>= 1, m >>= 1)
-#pragma unroll
-                    for (int i = 0; i < m; ++i) {
-                        const bool up = (lane & o) != 0;
-                        const float keep = up ? acc[i + m] : acc[i], send = up ? acc[i] : acc[i + m];
-                        acc[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-                    }
-#pragma unroll
-                for (int o = 16 / NT; o > 0; o >>= 1) acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], o);
-                const int t = lane / (32 / NT);
-                if (lane % (32 / NT) == 0 && t < cnt) part[t * p.r + k] += acc[0];
             }
+            // transposing reduction: after it, lane l holds sum l * KF * NT / 32
+            constexpr int S = KF * NT;
+#pragma unroll
+            for (int o = 16, m = S / 2; m > 0; o >>= 1, m >>= 1)
+#pragma unroll
+                for (int i = 0; i < m; ++i) {
+                    const bool up = (lane & o) != 0;
+                    const float keep = up ? acc[i + m] : acc[i], send = up ? acc[i] : acc[i + m];
+                    acc[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+                }
+#pragma unroll
+            for (int o = 16 / S; o > 0; o >>= 1) acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], o);
+            const int mine = lane / (32 / S), t = mine % NT, k = k0 + 8 * sharing * (mine / NT);
+            if (lane % (32 / S) == 0 && t < cnt && k < p.r) part[t * p.r + k] += acc[0];
         }
     }
 }
@@ -191,6 +190,7 @@ __device__ __forceinline__ void expand_columns(const W* b, const AdapterArgs& p,
         br[t] = p.base ? p.base + row * p.ldb : nullptr;
         yr[t] = p.y + row * p.ldy;
     }
+    constexpr int KF = sizeof(W) == 4 ? 2 : 4;
     for (int64_t n = n0; n < n1; n += COLS) {
         const W* row = b + n * p.r;
         float acc[NT], bv[NT];
@@ -199,13 +199,18 @@ __device__ __forceinline__ void expand_columns(const W* b, const AdapterArgs& p,
             acc[t] = 0.0f;
             bv[t] = (t < cnt && p.base) ? br[t][n] : 0.0f;
         }
-#pragma unroll 4
-        for (int k = 0; k < p.r; k += 8) {
-            float w[8];
-            load8(row + k, w);
+        for (int k0 = 0; k0 < p.r; k0 += 8 * KF) {
+            Raw8<W> raw[KF];
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
-                if (t < cnt) {
+            for (int j = 0; j < KF; ++j) raw[j].load(row + min(k0 + 8 * j, p.r - 8));
+#pragma unroll
+            for (int j = 0; j < KF; ++j) {
+                const int k = k0 + 8 * j;
+                if (k >= p.r) break;  // uniform
+                float w[8];
+                raw[j].unpack(w);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {  // (u of rows from cnt on is zero)
                     const float4 c = *reinterpret_cast<const float4*>(u + t * p.r + k);
                     const float4 d = *reinterpret_cast<const float4*>(u + t * p.r + k + 4);
                     acc[t] = fmaf(w[0], c.x, acc[t]); acc[t] = fmaf(w[1], c.y, acc[t]);
@@ -213,6 +218,7 @@ __device__ __forceinline__ void expand_columns(const W* b, const AdapterArgs& p,
                     acc[t] = fmaf(w[4], d.x, acc[t]); acc[t] = fmaf(w[5], d.y, acc[t]);
                     acc[t] = fmaf(w[6], d.z, acc[t]); acc[t] = fmaf(w[7], d.w, acc[t]);
                 }
+            }
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t)
@@ -326,10 +332,16 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(THREADS, 4)
         }
         reinterpret_cast<float4*>(s_u)[i] = make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale);
     }
+    if (cnt > 1)
+        for (int i = cnt * p.r + tid; i < ROWS * p.r; i += THREADS) s_u[i] = 0.0f;
     cluster_arrive();  // (this CTA has read the others' parts)
     __syncthreads();
     if (cnt == 1)
         expand_columns<W, 1>(b, p, s_tok, cnt, s_u, n0, n1);
+    else if (cnt == 2)
+        expand_columns<W, 2>(b, p, s_tok, cnt, s_u, n0, n1);
+    else if (cnt <= 4)
+        expand_columns<W, 4>(b, p, s_tok, cnt, s_u, n0, n1);
     else
         expand_columns<W, 8>(b, p, s_tok, cnt, s_u, n0, n1);
     cluster_wait();  // (the others have read this CTA's part)
@@ -1210,13 +1222,15 @@ cudaError_t launch_tiles(const AdapterArgs& p, cudaStream_t s) {
 
 // The choice of kernel and of the tile kernel's cluster, by what the steps of
 // either were measured to take (us; H = 256 .. 2048, N = 300 .. 16384):
-//   rows: 9 + 3e-6 * tiles of 8 rows * r (H + N);
-//   tiles: 5 + waves * (4 + 0.6 a panel of H + 2 a block of y, per CTA), one CTA
-//   an SM (about 12 of 13 SMs can hold clusters of 4, and 15 clusters of 8 fit).
-// (2048 -> 2048, rank 16, 4 adapters: 256 rows 13.9 us as rows, 17.9 as tiles;
-// 512 rows 23.9 and 18.7.  Rank 64: 128 rows 27.7 and 21.0.)  A cluster must be
-// wide enough that an accumulator of step 1 sums no more than CHAIN panels:
-// each addition truncates, and 4 CHAIN of them drift by about 1e-6 of the sum.
+//   rows: 9 + 0.08 a tile of 8 rows + 0.9e-6 r (H + N) a tile;
+//   tiles: 4 + waves * (4 + 0.05 r + 0.6 a panel of H + 2 a block of y, per CTA),
+//   one CTA an SM (about 12 of 13 SMs can hold clusters of 4, and 15 clusters of
+//   8 fit).
+// (2048 -> 2048, 4 adapters, rank 16: 512 rows 15.6 us as rows, 18.8 as tiles;
+// 1024 rows 25.9 and 19.8.  Rank 64: 256 rows 18.3 and 21.5; 512 rows 26.1 and
+// 22.3.)  A cluster must be wide enough that an accumulator of step 1 sums no
+// more than CHAIN panels: each addition truncates, and 4 CHAIN of them drift by
+// about 1e-6 of the sum.
 template <class W>
 cudaError_t launch_typed(const AdapterArgs& p, const DeviceInfo& dev, cudaStream_t s) {
     constexpr int CHAIN = 10;
@@ -1226,13 +1240,14 @@ cudaError_t launch_typed(const AdapterArgs& p, const DeviceInfo& dev, cudaStream
     const auto tiles = [&](int rows) {
         return (double)(p.T < (int64_t)rows * (p.n + 1) ? std::min<int64_t>(p.T, p.n + 1) : p.T / rows + (p.n + 1) / 2);
     };
-    double best = 9.0 + 3e-6 * std::min<double>((double)p.T, (double)(p.T / ROWS + (p.n + 1) / 2)) * p.r * (double)(p.H + p.N);
+    const double small = std::min<double>((double)p.T, (double)(p.T / ROWS + (p.n + 1) / 2));
+    double best = 9.0 + small * (0.08 + 0.9e-6 * p.r * (double)(p.H + p.N));
     int cl = 0;
     for (int c = 1; c <= CL; c *= 2) {
         if (chunks > c * accs * CHAIN) continue;
         const int slots = c <= 2 ? dev.sm_count : c == 4 ? dev.sm_count * 12 / 13 : 15 * CL * dev.sm_count / 148;
-        const double t = 5.0 + std::ceil(tiles(TM) * c / slots) *
-                                   (4.0 + 0.6 * chunks / c + 2.0 * (double)ceil_div(ceil_div(p.N, TM), c));
+        const double t = 4.0 + std::ceil(tiles(TM) * c / slots) *
+                                   (4.0 + 0.05 * p.r + 0.6 * chunks / c + 2.0 * (double)ceil_div(ceil_div(p.N, TM), c));
         if (t < best) {
             best = t;
             cl = c;

@@ -80,7 +80,13 @@ def check(A, x, e, base, y):
     (8, 2048, 5000, 128, 8, "mixed"), (9, 1024, 700, 40, 1, "one"), (63, 2048, 1001, 64, 5, "mixed"),
     (64, 512, 300, 56, 64, "mixed"), (65, 512, 300, 56, 64, "mixed"), (127, 1280, 257, 120, 2, "runs"),
     (129, 2560, 130, 96, 1, "one"), (300, 2048, 1000, 32, 1000, "mixed"), (513, 256, 129, 8, 3, "runs"),
-    (947, 2048, 2048, 64, 4, "runs"), (1100, 768, 1001, 128, 2, "mixed"), (2000, 1024, 640, 16, 1024, "mixed")])
+    (947, 2048, 2048, 64, 4, "runs"), (1100, 768, 1001, 128, 2, "mixed"), (2000, 1024, 640, 16, 1024, "mixed"),
+    # tiles in clusters of 8, 4, 2 and 1, one adapter or several, ranks with one to four panels
+    (1500, 512, 1500, 8, 2, "mixed"), (3000, 512, 300, 40, 2, "mixed"), (3000, 1024, 129, 128, 2, "runs"),
+    (7000, 512, 130, 64, 3, "runs"), (7000, 256, 1000, 96, 1, "one"), (18000, 512, 260, 16, 4, "mixed"),
+    (18000, 256, 64, 120, 1, "one"),
+    # sums too long for the tensor core's accumulators: the rows kernel, however many rows
+    (700, 16384, 100, 128, 1, "one"), (500, 16384, 100, 64, 2, "mixed")])
 def test_adapters_match_the_formula(kind, T, H, N, r, n, ids):
     A, x, e, base = make(T + N, T, H, N, r, n, kind, ids)
     check(A, x, e, base, m.moe_q4_adapters_apply(A, x, e, base=base))
@@ -175,6 +181,24 @@ def test_captured_and_on_another_stream(T):
             g.replay()
     torch.cuda.synchronize()
     assert torch.equal(y1, want) and torch.equal(y2, want)
+
+
+@pytest.mark.parametrize("T", [6, 260, 1200])
+def test_rows_past_32_bit_offsets(T):
+    """Pitches that put base's and y's rows more than 2^32 bytes from the first."""
+    A, x, e, base = make(19, T, 512, 200, 16, 2, "bf16", "mixed")
+    want = m.moe_q4_adapters_apply(A, x, e, base=base)
+    ld = (6 << 30) // 4 // T // 4 * 4 + 8
+    wide = torch.empty((T - 1) * ld + 200, device="cuda")   # 6 GB
+    y = wide.as_strided((T, 200), (ld, 1))
+    y.copy_(base)
+    m.moe_q4_adapters_apply(A, x, e, base=y, y=y)
+    assert torch.equal(y, want)
+    xw = torch.empty((T - 1) * ld + 512, device="cuda").as_strided((T, 512), (ld, 1))
+    xw.copy_(x)
+    y.zero_()
+    m.moe_q4_adapters_apply(A, xw, e, base=base, y=y)
+    assert torch.equal(y, want)
 
 
 def test_no_rows():
