@@ -32,7 +32,7 @@ namespace {
 constexpr int CL = 8;             // CTAs per cluster
 constexpr int THREADS = 256;
 constexpr int ROWS = 8;           // rows per tile of the rows kernel
-constexpr int INLINE_T = 64;      // up to this many rows are grouped inside the kernel
+constexpr int INLINE_T = 256;     // up to this many rows are grouped inside the kernel (a thread each)
 constexpr int COLS = CL * THREADS;  // columns of y that a cluster covers at a time
 constexpr int GROUP_THREADS = 1024;
 constexpr int GROUP_IDS = 16;     // ids per thread of the grouping kernels
@@ -234,8 +234,8 @@ __device__ __forceinline__ void expand_columns(const W* b, const AdapterArgs& p,
 template <class W, bool INLINE>
 __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(THREADS, 4)
     adapters_rows_kernel(const __grid_constant__ AdapterArgs p, int chunks, int iters) {
-    __shared__ int s_ids[INLINE_T];
-    __shared__ int s_starts[2];
+    __shared__ __align__(16) int s_ids[THREADS];
+    __shared__ int s_starts[THREADS / 32];
     __shared__ int s_tok[ROWS];
     __shared__ int s_group[3];  // adapter, rank of its first row among its adapter's rows, rows
     __shared__ __align__(16) float s_part[ROWS * 128];
@@ -249,31 +249,38 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(THREADS, 4)
         // groups in the order of their first rows
         const int T = (int)p.T;
         if (tid < 3) s_group[tid] = 0;
+        static_assert(INLINE_T <= THREADS);
         int e = -2;
         bool bad = false;
-        if (tid < INLINE_T) {
-            if (tid < T) {
-                e = __ldg(p.ids + tid);
-                bad = e < -1 || e >= p.n;
-                if (bad) e = -1;
-            }
-            s_ids[tid] = e;
+        if (tid < T) {
+            e = __ldg(p.ids + tid);
+            bad = e < -1 || e >= p.n;
+            if (bad) e = -1;
         }
+        s_ids[tid] = e;
         const int any = __syncthreads_or(bad);
         // the status word is written, not OR-ed, by one CTA
         if (blockIdx.x == 0 && tid == 0) *p.status = any ? STATUS_BAD_ADAPTER_INDEX : 0u;
-        int r = 0;
-        bool start = false;
-        unsigned starts = 0;
-        if (tid < INLINE_T) {
-            for (int i = 0; i < INLINE_T; ++i) r += (i < tid && s_ids[i] == e) ? 1 : 0;
-            start = tid < T && r % ROWS == 0;
-            starts = __ballot_sync(0xffffffffu, start);
-            if (lane == 0) s_starts[warp] = __popc(starts);
-        }
+        // this row's rank among the rows of its adapter: in its warp, and in the warps before
+        int r = __popc(__match_any_sync(0xffffffffu, e) & ((1u << lane) - 1u));
+        for (int w = 0; w < warp && tid - lane < T; ++w)
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+                const int4 q = *reinterpret_cast<const int4*>(s_ids + 32 * w + i);
+                r += (q.x == e) + (q.y == e) + (q.z == e) + (q.w == e);
+            }
+        const bool start = tid < T && r % ROWS == 0;
+        const unsigned starts = __ballot_sync(0xffffffffu, start);
+        if (lane == 0) s_starts[warp] = __popc(starts);
         __syncthreads();
-        if (g >= s_starts[0] + s_starts[1]) return;  // uniform over the cluster
-        if (start && (warp ? s_starts[0] : 0) + __popc(starts & ((1u << lane) - 1u)) == g) {
+        int before = 0, groups = 0;
+#pragma unroll
+        for (int w = 0; w < THREADS / 32; ++w) {
+            before += w < warp ? s_starts[w] : 0;
+            groups += s_starts[w];
+        }
+        if (g >= groups) return;  // uniform over the cluster
+        if (start && before + __popc(starts & ((1u << lane) - 1u)) == g) {
             s_group[0] = e;
             s_group[1] = r;
         }

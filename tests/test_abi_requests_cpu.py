@@ -100,11 +100,11 @@ def test_adapters_calls_that_pass_the_checks(lib):
 
 def test_adapters_workspace_grows_with_the_rows(lib):
     A = adapters()
-    got = [lib.moe_q4_adapters_workspace_bytes(ctypes.byref(A), T) for T in (0, 1, 64, 65, 1000, 16384, 16385, 1 << 24)]
-    assert got[0] == got[1] == got[2] == 256 and all(b >= a for a, b in zip(got, got[1:])) and got[3] > 65 * 4
+    got = [lib.moe_q4_adapters_workspace_bytes(ctypes.byref(A), T) for T in (0, 1, 256, 257, 1000, 16384, 16385, 1 << 24)]
+    assert got[0] == got[1] == got[2] == 256 and all(b >= a for a, b in zip(got, got[1:])) and got[3] > 257 * 4
     assert lib.moe_q4_adapters_workspace_bytes(ctypes.byref(A), -1) == 0
     assert lib.moe_q4_adapters_workspace_bytes(ctypes.byref(A), (1 << 24) + 1) == 0
-    assert apply(lib, A, T=65, nbytes=got[3] - 1) == -4
+    assert apply(lib, A, T=257, nbytes=got[3] - 1) == -4
 
 
 L, OUT, TOK, LSE, ST = (FAKE + k * G for k in (0, 1, 2, 3, 4))

@@ -79,7 +79,8 @@ def check(A, x, e, base, y):
     (1, 2048, 2048, 16, 4, "one"), (1, 256, 1, 8, 1, "one"), (1, 512, 33, 8, 3, "none"), (2, 768, 2049, 24, 2, "mixed"),
     (8, 2048, 5000, 128, 8, "mixed"), (9, 1024, 700, 40, 1, "one"), (63, 2048, 1001, 64, 5, "mixed"),
     (64, 512, 300, 56, 64, "mixed"), (65, 512, 300, 56, 64, "mixed"), (127, 1280, 257, 120, 2, "runs"),
-    (129, 2560, 130, 96, 1, "one"), (300, 2048, 1000, 32, 1000, "mixed"), (513, 256, 129, 8, 3, "runs"),
+    (129, 2560, 130, 96, 1, "one"), (255, 256, 40, 16, 300, "mixed"), (256, 768, 100, 8, 3, "mixed"), (257, 768, 100, 8, 3, "mixed"),
+    (256, 512, 33, 24, 1, "one"), (257, 512, 33, 24, 200, "mixed"), (300, 2048, 1000, 32, 1000, "mixed"), (513, 256, 129, 8, 3, "runs"),
     (947, 2048, 2048, 64, 4, "runs"), (1100, 768, 1001, 128, 2, "mixed"), (2000, 1024, 640, 16, 1024, "mixed"),
     # tiles in clusters of 8, 4, 2 and 1, one adapter or several, ranks with one to four panels
     (1500, 512, 1500, 8, 2, "mixed"), (3000, 512, 300, 40, 2, "mixed"), (3000, 1024, 129, 128, 2, "runs"),
