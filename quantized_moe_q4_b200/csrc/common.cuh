@@ -38,9 +38,6 @@ constexpr uint32_t STATUS_SCALE_OVERFLOW = 0x1u;
 constexpr uint32_t STATUS_SPIN_TIMEOUT = 0x2u;
 constexpr uint32_t STATUS_NONFINITE_LOGIT = 0x4u;
 constexpr uint32_t STATUS_BAD_EXPERT_INDEX = 0x8u;
-constexpr uint32_t STATUS_BAD_ADAPTER_INDEX = 0x10u;
-constexpr uint32_t STATUS_BAD_MASK_INDEX = 0x20u;
-constexpr uint32_t STATUS_NAN_LOGIT = 0x40u;
 
 // ---------------------------------------------------------------------------
 // Scalar rules

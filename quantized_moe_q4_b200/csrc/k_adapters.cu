@@ -20,6 +20,7 @@
 #include <cmath>
 #include <type_traits>
 
+#include "cluster.cuh"
 #include "common.cuh"
 #include "launch.h"
 #include "ptx.cuh"
@@ -38,40 +39,6 @@ constexpr int GROUP_THREADS = 1024;
 constexpr int GROUP_IDS = 16;     // ids per thread of the grouping kernels
 constexpr int GROUP_CHUNK = GROUP_THREADS * GROUP_IDS;
 constexpr int MAX_ADAPTERS = 1024;
-
-// ------------------------------------------------------------------ clusters
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-
-// Address of the same shared variable in CTA `rank` of the cluster.
-__device__ __forceinline__ uint32_t map_rank(uint32_t smem_addr, uint32_t rank) {
-    uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr), "r"(rank));
-    return a;
-}
-__device__ __forceinline__ void st_cluster4(uint32_t addr, float4 v) {
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
-                 : "memory");
-}
-__device__ __forceinline__ int ld_cluster1(uint32_t addr) {
-    int v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-    return v;
-}
-__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
-}
 
 // ------------------------------------------------------------------ weights
 
@@ -118,8 +85,6 @@ struct Raw8<float> {
         for (int i = 0; i < 8; ++i) v[i] = v_[i];
     }
 };
-
-__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // ------------------------------------------------------------------ rows kernel
 
@@ -295,8 +260,9 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(THREADS, 4)
         cnt = s_group[2];
     } else {
         pdl_wait();
-        if (g >= *p.n_tiles) return;
-        const int4 tile = p.tiles[g];
+        const int n_tiles = *p.n_tiles;
+        const int4 tile = p.tiles[g];  // (not one of them, perhaps, but in the workspace; both loads at once)
+        if (g >= n_tiles) return;
         id = tile.x;
         cnt = tile.z;
         if (tid < cnt) s_tok[tid] = p.perm[tile.y + tid];
@@ -566,8 +532,9 @@ __global__ void __launch_bounds__(TT, 1) adapters_tile_kernel(const __grid_const
     }
     pdl_wait();
     const int g = (int)(blockIdx.x / CLT);
-    if (g >= *p.n_tiles) return;  // uniform over the cluster
-    const int4 tile = p.tiles[g];
+    const int n_tiles = *p.n_tiles;
+    const int4 tile = p.tiles[g];  // (not one of them, perhaps, but in the workspace; both loads at once)
+    if (g >= n_tiles) return;      // uniform over the cluster
     const int id = tile.x, cnt = tile.z;
     if (tid < TM) {
         const int t = tid < cnt ? p.perm[tile.y + tid] : -1;

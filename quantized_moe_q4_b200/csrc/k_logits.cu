@@ -23,6 +23,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "cluster.cuh"
 #include "common.cuh"
 #include "launch.h"
 #include "ptx.cuh"
@@ -77,8 +78,6 @@ __device__ __forceinline__ Best join_lanes(Best b, int n) {
     }
     return b;
 }
-
-__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 struct Row {
     float rep, pres, freq;
@@ -136,12 +135,11 @@ __global__ void __launch_bounds__(THREADS, 2) logits_kernel(const __grid_constan
     __shared__ Best s_cl[MAX_CL];
     __shared__ int s_dup, s_seen;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    uint32_t rank;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    const uint32_t rank = cluster_rank();
     const int64_t t = blockIdx.x >> lg;
     const bool pick = p.token || p.lse;
     const float NEG = __int_as_float(0xff800000);
-    if (pick) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    if (pick) cluster_arrive();
     uint32_t* words = s_mem + (p.mask ? (slice / 32 + 3) / 4 * 4 : 0);
     uint32_t* ruled = words + slice;
     uint32_t* listed = ruled + slice / 32;
@@ -415,21 +413,20 @@ __global__ void __launch_bounds__(THREADS, 2) logits_kernel(const __grid_constan
     }
     if (lane == 0) s_best[warp] = best;
     __syncthreads();
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cluster_wait();
     if (warp == 0) {
         best = join_lanes(s_best[lane & (WARPS - 1)], WARPS);
         if (lane == 0) {
-            uint32_t a;
-            asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(&s_cl[rank])));
-            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(best.m) : "memory");
-            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a + 4), "r"(best.i) : "memory");
-            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a + 8), "f"(best.s) : "memory");
+            const uint32_t a = map_rank(smem_u32(&s_cl[rank]), 0);
+            st_cluster(a, best.m);
+            st_cluster(a + 4, __int_as_float(best.i));
+            st_cluster(a + 8, best.s);
         }
         __syncwarp();
     }
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    cluster_arrive();
     if (rank != 0) return;  // (nobody reads this CTA's memory)
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cluster_wait();
     if (warp == 0) {
         best = lane < (1 << lg) ? s_cl[lane] : Best{NEG, 0x7fffffff, 0.0f};
         best = join_lanes(best, MAX_CL);
