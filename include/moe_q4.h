@@ -273,12 +273,14 @@ int moe_q4_gemv(const uint8_t* W, int64_t N, int32_t H, const float* x, int64_t 
  *     in place, rows without an adapter are then neither read nor written.
  *   - adapter [T] int32 on the device, in any order; an index outside
  *     [-1, n_adapters) counts as -1 and sets MOE_Q4_STATUS_BAD_ADAPTER_INDEX.
- *   - a and b are fp32, binary16 or bfloat16 (dtype), never rounded; x and
- *     A x keep 22 significant bits or more and all sums are fp32.  A lower
+ *   - a and b are fp32, binary16 or bfloat16 (dtype).  x, A x and fp32
+ *     adapters keep 21 significant bits or more in every product (all of
+ *     them in small batches), and all sums are fp32.  A lower
  *     rank than `rank` is stored with zero rows of a / columns of b.
- *   - A row's result depends on that row and its adapter, on T through the
- *     choice of kernel, and on nothing else in the batch; the same call gives
- *     the same bits.
+ *   - A row's result depends on that row and its adapter, on the shapes (T
+ *     among them) through the choice of kernel, and on no other row; the same
+ *     call gives the same bits.  x must be finite (a row that is not spoils
+ *     itself only).
  *   - hidden a positive multiple of 256 up to 16384; rank a multiple of 8,
  *     8 <= rank <= 128 (else MOE_Q4_ERR_SHAPE); 1 <= n_out <= 2^30;
  *     1 <= n_adapters <= 1024.  x, a, b 16-byte aligned, the other arrays

@@ -404,7 +404,7 @@ def _rows(t: torch.Tensor, name: str, device: int, rows: int, cols: int) -> int:
     pitch, step = t.stride()
     if step != 1 and cols > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return pitch if rows > 1 else max(pitch, cols)
+    return pitch if rows > 1 else cols  # (of a single row it does not matter)
 
 
 def _vector(t, name: str, device: int, dtype, n=None):

@@ -125,15 +125,16 @@ __device__ __forceinline__ void each_token(const int32_t* list, int64_t lo, int6
 // Dynamic shared memory: allowed[slice / 32] (the mask's words), and for rows
 // with histories or biases words[slice] (history word, or for a ruled token
 // the bits of its logit), ruled[slice / 32] (bit set: the word is such a
-// logit), listed[slice / 32] (bit set: a bias lists the token), seen[slice]
-// (16-bit: the places of the history's tokens).  Place i of a CTA's `slice`
+// logit), listed[slice / 32] (bit set: a bias lists the token), twice[slice /
+// 32] (bit set: more than once), seen[slice] (16-bit: the places of the
+// history's tokens).  Place i of a CTA's `slice`
 // (a multiple of 32) is token base + 32 * (i / 32 * ncl + rank) + i % 32, with
 // ncl = 1 << lg CTAs in the cluster.
 __global__ void __launch_bounds__(THREADS, 2) logits_kernel(const __grid_constant__ LogitArgs p, int slice, int lg) {
     extern __shared__ __align__(16) uint32_t s_mem[];
     __shared__ Best s_best[WARPS];
     __shared__ Best s_cl[MAX_CL];
-    __shared__ int s_dup, s_seen;
+    __shared__ int s_seen;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = cluster_rank();
     const int64_t t = blockIdx.x >> lg;
@@ -143,7 +144,8 @@ __global__ void __launch_bounds__(THREADS, 2) logits_kernel(const __grid_constan
     uint32_t* words = s_mem + (p.mask ? (slice / 32 + 3) / 4 * 4 : 0);
     uint32_t* ruled = words + slice;
     uint32_t* listed = ruled + slice / 32;
-    uint16_t* seen = reinterpret_cast<uint16_t*>(listed + slice / 32);
+    uint32_t* twice = listed + slice / 32;
+    uint16_t* seen = reinterpret_cast<uint16_t*>(twice + slice / 32);
     const float* in = p.logits + t * p.ld;
     float* out = p.out ? p.out + t * p.ldo : nullptr;
     const auto token_at = [&](uint32_t i) { return (((i >> 5 << lg) + rank) << 5) + (i & 31); };  // less base
@@ -207,8 +209,8 @@ __global__ void __launch_bounds__(THREADS, 2) logits_kernel(const __grid_constan
                 row.freq = p.freq ? __ldg(p.freq + t) : 0.0f;
                 if (h1 > h0)
                     for (int i = tid; i < len / 4; i += THREADS) reinterpret_cast<uint4*>(words)[i] = make_uint4(0, 0, 0, 0);
-                for (int i = tid; i < len / 32; i += THREADS) ruled[i] = listed[i] = 0;
-                if (tid == 0) s_dup = s_seen = 0;
+                for (int i = tid; i < len / 32; i += THREADS) ruled[i] = listed[i] = twice[i] = 0;
+                if (tid == 0) s_seen = 0;
                 __syncthreads();
                 each_token(p.tokens, h0, h1, [&](int v, int64_t at) {
                     uint32_t i;
@@ -224,7 +226,7 @@ __global__ void __launch_bounds__(THREADS, 2) logits_kernel(const __grid_constan
                     uint32_t i;
                     if (!inside(__ldg(p.bias_token + e), i)) continue;
                     const uint32_t bit = 1u << (i & 31);
-                    if (atomicOr(&listed[i >> 5], bit) & bit) s_dup = 1;
+                    if (atomicOr(&listed[i >> 5], bit) & bit) atomicOr(&twice[i >> 5], bit);
                     if (e == b0 + tid) {
                         bias_at = i;
                         bias_logit = src[token_at(i)];
@@ -265,11 +267,11 @@ __global__ void __launch_bounds__(THREADS, 2) logits_kernel(const __grid_constan
                         const int v = __ldg(p.bias_token + e);
                         uint32_t i;
                         if (!inside(v, i)) continue;
+                        const uint32_t bit = 1u << (i & 31);
                         bool last = true;  // the later entry of a token listed twice counts
-                        if (s_dup)
+                        if (twice[i >> 5] & bit)
                             for (int64_t f = e + 1; f < b1 && last; ++f) last = __ldg(p.bias_token + f) != v;
                         if (!last) continue;
-                        const uint32_t bit = 1u << (i & 31);
                         const bool set = atomicOr(&ruled[i >> 5], bit) & bit;
                         const float l = set ? __uint_as_float(words[i]) : kept ? bias_logit : src[token_at(i)];
                         words[i] = __float_as_uint(__fadd_rn(l, kept ? bias_add : __ldg(p.bias_value + e)));
@@ -462,7 +464,7 @@ cudaError_t launch_logits(const LogitArgs& p, const DeviceInfo& dev, cudaStream_
     int64_t slice = ceil_div(ceil_div(p.V, ncl), 32) * 32;
     if (slice > MAX_SLICE) slice = MAX_SLICE;
     const bool sparse = p.row_start || p.bias_start;
-    const size_t smem = (p.mask ? ((size_t)slice / 32 + 3) / 4 * 16 : 0) + (sparse ? 4 * (size_t)slice + (size_t)slice / 4 + 2 * (size_t)slice : 0);
+    const size_t smem = (p.mask ? ((size_t)slice / 32 + 3) / 4 * 16 : 0) + (sparse ? 6 * (size_t)slice + 3 * (size_t)slice / 8 : 0);
     int per_sm = 0;
     cudaError_t e = kernel_occupancy(reinterpret_cast<const void*>(logits_kernel), THREADS, smem, &per_sm);
     if (e != cudaSuccess) return e;

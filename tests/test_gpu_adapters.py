@@ -5,11 +5,13 @@ Tolerance.  With u = 2^-24, a sum of products computed in binary32 is off by
 at most c * u * (sum of the products' magnitudes), where c counts the
 roundings a term passes through.  Rows kernel: a lane adds H/32 products, 5
 shuffles join the lanes, up to 8 parts join, r products follow, then the
-scale and the base: H/32 + r + 16.  Tile kernel: x and A x as two tf32 parts
-of 11 bits each (2 * 2^-22, 8 u, each once), H/64 + 8 accumulations of 8-wide
-steps for each of two parts, each truncated (2 u), 8 parts joined, then 2 r/8
-of them again.  Both are under C = H/16 + 2 r + 64 times u S, with S = |base| +
-|scale| sum_k |B_k| sum_h |A_kh x_h|.
+scale and the base: H/32 + r + 16.  Tile kernel: x, A x and binary32 weights as
+two tf32 parts of 11 bits (2^-21 = 8 u, each once, so 24 u, and 4 u for the
+product of two lo parts that is left out), H/8 accumulations of 8-wide steps
+spread over the CTAs and accumulators, each truncated (2 u) -- at most 40 in a
+row --, up to 16 accumulators and 8 parts joined, then r/8 accumulations again.
+Both are under C = H/16 + 2 r + 64 times u S, with S = |base| + |scale| sum_k
+|B_k| sum_h |A_kh x_h|.
 """
 import numpy as np
 import pytest
@@ -93,9 +95,9 @@ def test_adapters_match_the_formula(kind, T, H, N, r, n, ids):
     check(A, x, e, base, m.moe_q4_adapters_apply(A, x, e, base=base))
 
 
-@pytest.mark.parametrize("T", [20000, 40000])
-def test_many_rows_in_several_grouping_chunks(T):
-    A, x, e, base = make(T, T, 256, 40, 16, 7, "bf16", "mixed")
+@pytest.mark.parametrize("T,n", [(2049, 3), (20000, 7), (40000, 1024), (131073, 5), (140000, 1023)])
+def test_many_rows_in_several_grouping_chunks(T, n):
+    A, x, e, base = make(T, T, 256, 24, 8, n, "bf16", "mixed")
     check(A, x, e, base, m.moe_q4_adapters_apply(A, x, e, base=base))
 
 
@@ -121,7 +123,7 @@ def test_pitches_in_place_no_base_no_scale(T):
     assert torch.equal(both[:, 512:813], y) and bool((both[:, 813:] == 0).all())
 
 
-@pytest.mark.parametrize("T", [7, 64, 200, 1000])
+@pytest.mark.parametrize("T", [7, 64, 200, 1000, 5000, 140000])
 def test_bad_indices_are_reported_and_count_as_none(T):
     A, x, e, base = make(5, T, 256, 100, 8, 3, "fp16", "mixed")
     ws = m.alloc_workspace(m.moe_q4_adapters_workspace_bytes(A, T))

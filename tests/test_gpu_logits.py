@@ -181,6 +181,16 @@ def test_padding_tokens_duplicate_and_foreign_biases():
     assert all(np.array_equal(x, y) for x, y in zip(a[:3], b[:3]))
 
 
+def test_a_long_list_of_biases_with_two_of_a_token_far_apart():
+    V = 50000
+    d = make(12, 3, V, 30, 0, 0)
+    rng = np.random.default_rng(1)
+    tok = np.concatenate([rng.permutation(V), rng.permutation(V)[:300]]).astype(np.int32)
+    d["bias_token"], d["bias_value"] = tok, rng.standard_normal(len(tok)).astype(np.float32)
+    d["bias_start"] = np.array([0, 0, len(tok), len(tok)], np.int64)
+    check(d, apply(d))
+
+
 def test_start_positions_outside_their_lists_are_clamped():
     d = make(5, 4, 500, 20, 5, 0)
     d["row_start"] = np.array([-5, 3, 10, 2 ** 60, 2 ** 62], np.int64)
