@@ -1030,7 +1030,7 @@ __device__ __forceinline__ void scan_groups(const AdapterArgs& p, int tile_rows,
 template <int CLG>
 __global__ void __launch_bounds__(GROUP_THREADS)
     adapters_group_kernel(const __grid_constant__ AdapterArgs p, int tile_rows, int per) {
-    __shared__ int cnt[MAX_ADAPTERS + 2], all[MAX_ADAPTERS + 2], off[MAX_ADAPTERS + 2], toff[MAX_ADAPTERS + 2];
+    __shared__ int cnt[MAX_ADAPTERS + 2], all[MAX_ADAPTERS + 2], pre[MAX_ADAPTERS + 2], off[MAX_ADAPTERS + 2], toff[MAX_ADAPTERS + 2];
     pdl_launch_dependents();
     const int rank = CLG == 1 ? 0 : (int)cluster_rank();
     const int64_t first = (int64_t)rank * per, last = CLG == 1 ? p.T : min(p.T, first + per);
@@ -1056,21 +1056,19 @@ __global__ void __launch_bounds__(GROUP_THREADS)
                 sum += v;
             }
             all[i] = sum;
-            toff[i] = before;
+            pre[i] = before;
         }
-        cluster_arrive();
-        cluster_wait();  // (every CTA has read the counts)
-        for (int i = threadIdx.x; i < p.n + 1; i += GROUP_THREADS) cnt[i] = toff[i];
+        cluster_arrive();  // (this CTA has read the others' counts)
         __syncthreads();
         scan_groups(p, tile_rows, all, off, toff, rank, CLG);
-        for (int i = threadIdx.x; i < p.n + 1; i += GROUP_THREADS) off[i] += cnt[i];
-        __syncthreads();
     }
 #pragma unroll
     for (int i = 0; i < GROUP_IDS; ++i)
-        if (grp[i] >= 0) p.perm[off[grp[i]] + rnk[i]] = (int32_t)(first + i * GROUP_THREADS + threadIdx.x);
+        if (grp[i] >= 0)
+            p.perm[off[grp[i]] + (CLG == 1 ? 0 : pre[grp[i]]) + rnk[i]] = (int32_t)(first + i * GROUP_THREADS + threadIdx.x);
     const int* total = CLG == 1 ? cnt : all;
     if (rank == 0 && threadIdx.x == 0) *p.status = total[p.n + 1] ? STATUS_BAD_ADAPTER_INDEX : 0u;
+    if constexpr (CLG > 1) cluster_wait();  // (the others have read this CTA's counts)
 }
 
 // More rows: counts per chunk, offsets of every (chunk, group), placement.
