@@ -589,7 +589,8 @@ __global__ void __launch_bounds__(TT, 1) adapters_tile_kernel(const __grid_const
     const int64_t mine = (int64_t)rank < blocks ? (blocks - rank + CLT - 1) / CLT : 0;
     const int panels = (r + PK - 1) / PK, half = (panels + 1) / 2;       // of B; from `half` on a second accumulator
     const int n16 = (r + 15) / 16 * 16;
-    const int accs = min(MAX_ACCS, (int)COLS_TMEM / n16 - 1);  // accumulators of the hi products; the lo ones' comes after them
+    // accumulators of the hi products (one for every four panels, as far as TMEM has them); the lo ones' comes after them
+    const int accs = min(min(MAX_ACCS, (int)COLS_TMEM / n16 - 1), (chunks + 3) / 4);
 
     if (warp >= ROW_WARPS + WEIGHT_WARPS) {
         // ---------------- MMA (the whole warp waits, one lane issues)
@@ -784,16 +785,21 @@ __global__ void __launch_bounds__(TT, 1) adapters_tile_kernel(const __grid_const
     for (int c = warp >> 2; c < r / 8; c += ROW_WARPS / 4) {
         const uint32_t at = s_tmem + (uint32_t)((quad * 32) << 16) + 8u * c;
         float sum[8];
-        uint32_t v[8];
-        tmem_ld8(at + (uint32_t)(accs * n16), v);  // the small products first
+        uint32_t v[3][8];
+        tmem_ld8(at + (uint32_t)(accs * n16), v[0]);  // the small products first
         tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum[j] = __uint_as_float(v[j]);
-        for (int q = 0; q < accs && q < chunks; ++q) {
-            tmem_ld8(at + (uint32_t)(q * n16), v);
+        for (int j = 0; j < 8; ++j) sum[j] = __uint_as_float(v[0][j]);
+        for (int q = 0; q < accs; q += 3) {
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+                if (q + i < accs) tmem_ld8(at + (uint32_t)((q + i) * n16), v[i]);
             tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum[j] += __uint_as_float(v[j]);
+            for (int i = 0; i < 3; ++i)
+                if (q + i < accs)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) sum[j] += __uint_as_float(v[i][j]);
         }
         const int row = quad * 32 + lane;
         const float4 lo4 = make_float4(sum[0], sum[1], sum[2], sum[3]), hi4 = make_float4(sum[4], sum[5], sum[6], sum[7]);
