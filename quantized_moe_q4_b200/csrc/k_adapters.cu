@@ -34,6 +34,8 @@ constexpr int CL = 8;             // CTAs per cluster
 constexpr int THREADS = 256;
 constexpr int ROWS = 8;           // rows per tile of the rows kernel
 constexpr int INLINE_T = 256;     // up to this many rows are grouped inside the kernel (a thread each)
+constexpr int SCAN_T = 2048;      // up to this many rows of up to SCAN_N adapters, every CTA of either kernel can find
+constexpr int SCAN_N = 255;       // its tile by itself
 constexpr int COLS = CL * THREADS;  // columns of y that a cluster covers at a time
 constexpr int GROUP_THREADS = 1024;
 constexpr int GROUP_IDS = 16;     // ids per thread of the grouping kernels
@@ -83,6 +85,83 @@ struct Raw8<float> {
     __device__ __forceinline__ void unpack(float (&v)[8]) const {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = v_[i];
+    }
+};
+
+// ------------------------------------------------------------------ finding a tile
+//
+// Tile g of up to `tile_rows` rows, found by all NT threads of a CTA: counts of
+// the adapters' rows, their tiles' offsets, and the rows of the one adapter in
+// their order.  False: there is no tile g.  (p.T <= SCAN_T, p.n <= SCAN_N.)
+template <int NT>
+struct TileFinder {
+    static constexpr int K = (SCAN_T + NT - 1) / NT, WARPS = NT / 32;
+    int cnt[SCAN_N + 1], sums[WARPS], some[K * WARPS], found[3];
+
+    __device__ bool find(const AdapterArgs& p, int tile_rows, int g, int* tok, int& id, int& rows) {
+        const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, T = (int)p.T;
+        for (int i = tid; i <= p.n; i += NT) cnt[i] = 0;
+        if (tid == 0) found[0] = -1;
+        int grp[K];
+        bool bad = false;
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            const int t = j * NT + tid;
+            grp[j] = -1;
+            if (t < T) {
+                const int e = __ldg(p.ids + t);
+                const bool ok = (unsigned)e < (unsigned)p.n;
+                grp[j] = ok ? e : p.n;
+                bad |= !ok && e != -1;
+            }
+        }
+        const int any = __syncthreads_or(bad);
+        if (blockIdx.x + blockIdx.y == 0 && tid == 0) *p.status = any ? STATUS_BAD_ADAPTER_INDEX : 0u;
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            if (j * NT >= T) break;  // uniform
+            const unsigned peers = __match_any_sync(0xffffffffu, grp[j]);
+            if (grp[j] >= 0 && lane == __ffs(peers) - 1) atomicAdd(&cnt[grp[j]], __popc(peers));
+        }
+        __syncthreads();
+        // (in place, rows without an adapter need no tile)
+        const int c = tid <= p.n && !(tid == p.n && p.base == p.y) ? cnt[tid] : 0;
+        const int tiles = (c + tile_rows - 1) / tile_rows;
+        int incl = tiles;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int q = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += q;
+        }
+        if (lane == 31) sums[warp] = incl;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) incl += sums[w];
+        if (g >= incl - tiles && g < incl) {
+            found[0] = tid;
+            found[1] = (g - (incl - tiles)) * tile_rows;
+            found[2] = min(tile_rows, c - found[1]);
+        }
+        __syncthreads();
+        if (found[0] < 0) return false;
+        const int first = found[1];
+        id = found[0] < p.n ? found[0] : -1;
+        rows = found[2];
+        unsigned mine[K];
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            mine[j] = __ballot_sync(0xffffffffu, grp[j] == found[0]);
+            if (lane == 0) some[j * WARPS + warp] = __popc(mine[j]);
+        }
+        __syncthreads();
+        int before = 0, at = 0;
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            for (; at < j * WARPS + warp; ++at) before += some[at];
+            const int pos = before + __popc(mine[j] & ((1u << lane) - 1u)) - first;
+            if (grp[j] == found[0] && pos >= 0 && pos < rows) tok[pos] = j * NT + tid;
+        }
+        __syncthreads();
+        return true;
     }
 };
 
@@ -258,6 +337,9 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(THREADS, 4)
         __syncthreads();
         id = s_group[0];
         cnt = s_group[2];
+    } else if (p.scan) {
+        __shared__ TileFinder<THREADS> finder;
+        if (!finder.find(p, ROWS, g, s_tok, id, cnt)) return;  // uniform over the cluster
     } else {
         pdl_wait();
         const int n_tiles = *p.n_tiles;
@@ -530,14 +612,24 @@ __global__ void __launch_bounds__(TT, 1) adapters_tile_kernel(const __grid_const
         mbar_init(&s_u, ROW_WARPS);
         mbar_fence_init();
     }
-    pdl_wait();
     const int g = (int)(blockIdx.x / CLT);
-    const int n_tiles = *p.n_tiles;
-    const int4 tile = p.tiles[g];  // (not one of them, perhaps, but in the workspace; both loads at once)
-    if (g >= n_tiles) return;      // uniform over the cluster
-    const int id = tile.x, cnt = tile.z;
+    // the blocks of y of a tile go around the CTAs of all its clusters
+    const int first_n = (int)blockIdx.y * CLT + (int)rank, step_n = (int)gridDim.y * CLT;
+    int id, cnt;
+    if (p.scan) {
+        __shared__ TileFinder<TT> finder;
+        if (!finder.find(p, TM, g, s_tok, id, cnt)) return;  // uniform over the cluster
+    } else {
+        pdl_wait();
+        const int n_tiles = *p.n_tiles;
+        const int4 tile = p.tiles[g];  // (not one of them, perhaps, but in the workspace; both loads at once)
+        if (g >= n_tiles) return;      // uniform over the cluster
+        id = tile.x;
+        cnt = tile.z;
+        if (tid < cnt) s_tok[tid] = p.perm[tile.y + tid];
+    }
     if (tid < TM) {
-        const int t = tid < cnt ? p.perm[tile.y + tid] : -1;
+        const int t = tid < cnt ? s_tok[tid] : -1;
         s_tok[tid] = t;
         if (p.wide) {
             s_off[0][tid] = 4 * (int64_t)t * p.ldb;
@@ -550,17 +642,18 @@ __global__ void __launch_bounds__(TT, 1) adapters_tile_kernel(const __grid_const
     __syncthreads();
     if (id < 0) {  // no adapter (never in place: such rows have no tile then)
         constexpr int FLY = 16;
-        for (int t = (int)rank + CLT * warp; t < cnt; t += CLT * (TT / 32))
-            for (int64_t n = lane; n < p.N; n += 32 * FLY) {
-                const float* base = p.base + (int64_t)s_tok[t] * p.ldb + n;
-                float* y = p.y + (int64_t)s_tok[t] * p.ldy + n;
-                float v[FLY];
+        const int parts = (int)((p.N + 32 * FLY - 1) / (32 * FLY));  // of a row; a warp has one at a time
+        for (int64_t i = first_n + (int64_t)step_n * warp; i < (int64_t)cnt * parts; i += (int64_t)step_n * (TT / 32)) {
+            const int64_t t = s_tok[i % cnt], n = i / cnt * (32 * FLY) + lane;
+            const float* base = p.base + t * p.ldb + n;
+            float* y = p.y + t * p.ldy + n;
+            float v[FLY];
 #pragma unroll
-                for (int j = 0; j < FLY; ++j) v[j] = (p.base && n + 32 * j < p.N) ? base[32 * j] : 0.0f;
+            for (int j = 0; j < FLY; ++j) v[j] = (p.base && n + 32 * j < p.N) ? base[32 * j] : 0.0f;
 #pragma unroll
-                for (int j = 0; j < FLY; ++j)
-                    if (n + 32 * j < p.N) y[32 * j] = v[j];
-            }
+            for (int j = 0; j < FLY; ++j)
+                if (n + 32 * j < p.N) y[32 * j] = v[j];
+        }
         return;
     }
     if (warp == 0) tmem_alloc(&s_tmem, COLS_TMEM);
@@ -585,8 +678,8 @@ __global__ void __launch_bounds__(TT, 1) adapters_tile_kernel(const __grid_const
         }
     };
     const int chunks = p.H / CLT / PK, h0 = (int)rank * (p.H / CLT);  // this CTA's part of H
-    const int64_t blocks = (p.N + TM - 1) / TM;                          // its blocks of y: rank, rank + CLT, ...
-    const int64_t mine = (int64_t)rank < blocks ? (blocks - rank + CLT - 1) / CLT : 0;
+    const int blocks = (int)((p.N + TM - 1) / TM);                       // its blocks of y: first_n, first_n + step_n, ...
+    const int mine = first_n < blocks ? (blocks - first_n + step_n - 1) / step_n : 0;
     const int panels = (r + PK - 1) / PK, half = (panels + 1) / 2;       // of B; from `half` on a second accumulator
     const int n16 = (r + 15) / 16 * 16;
     // accumulators of the hi products (one for every four panels, as far as TMEM has them); the lo ones' comes after them
@@ -629,7 +722,7 @@ __global__ void __launch_bounds__(TT, 1) adapters_tile_kernel(const __grid_const
             tc_fence_after_sync();
             const uint32_t tmem = s_tmem;
             st = ph = 0;
-            for (int64_t i = 0; i < mine; ++i) {
+            for (int i = 0; i < mine; ++i) {
                 const uint32_t buf = (uint32_t)i & 1;
                 if (i >= 2) wait(&s_dempty[buf], (uint32_t)((i >> 1) - 1) & 1);
                 for (int k = 0; k < panels; ++k) {
@@ -667,8 +760,7 @@ __global__ void __launch_bounds__(TT, 1) adapters_tile_kernel(const __grid_const
             char* slot = sm + w * lay.slot;
             char* raw = sm + lay.raw + w * Panel<W>::BYTES;
             struct Cursor {
-                int64_t i;  // block of y
-                int k, h;   // its panel, part of the panel
+                int i, k, h;  // block of y, its panel, part of the panel
             };
             const auto step = [&](Cursor& c) {
                 if (++c.h < Panel<W>::PARTS) return;
@@ -677,7 +769,7 @@ __global__ void __launch_bounds__(TT, 1) adapters_tile_kernel(const __grid_const
             };
             const auto copy = [&](const Cursor& c) {
                 if (c.i >= mine) return;
-                const int64_t n0 = ((int64_t)rank + c.i * CLT) * TM;
+                const int64_t n0 = (int64_t)(first_n + c.i * step_n) * TM;
                 Panel<W>::copy(b + n0 * r + c.k * PK, r, (int)min((int64_t)TM, p.N - n0), r - c.k * PK, c.h, smem_u32(raw));
                 // the base under the block is needed soon after
                 if (c.k == 0 && c.h == 0 && p.base)
@@ -875,8 +967,8 @@ __global__ void __launch_bounds__(TT, 1) adapters_tile_kernel(const __grid_const
         const char* base = reinterpret_cast<const char*>(p.base);
         char* y = reinterpret_cast<char*>(p.y);
         float bv[2][16];
-        const auto load_base = [&](int64_t i, int h) {
-            const int64_t n = ((int64_t)rank + i * CLT) * TM + quad * 32 + lane;
+        const auto load_base = [&](int i, int h) {
+            const int n = (first_n + i * step_n) * TM + quad * 32 + lane;
             if (!base) {
 #pragma unroll
                 for (int j = 0; j < 16; ++j) bv[h][j] = 0.0f;
@@ -892,9 +984,9 @@ __global__ void __launch_bounds__(TT, 1) adapters_tile_kernel(const __grid_const
         };
         load_base(0, 0);
         load_base(0, 1);
-        for (int64_t i = 0; i < mine; ++i) {
+        for (int i = 0; i < mine; ++i) {
             const uint32_t buf = (uint32_t)i & 1;
-            const int64_t n = ((int64_t)rank + i * CLT) * TM + quad * 32 + lane;
+            const int n = (first_n + i * step_n) * TM + quad * 32 + lane;
             wait(&s_dfull[buf], (uint32_t)(i >> 1) & 1);
             tc_fence_after_sync();
             __syncwarp();
@@ -1130,7 +1222,7 @@ __global__ void __launch_bounds__(GROUP_THREADS) adapters_place_kernel(const __g
 // kernel before it drains (its kernels wait with pdl_wait before they read
 // anything).
 template <class... A>
-cudaError_t launch_clusters(void (*kernel)(A...), unsigned grid, int cluster, int threads, size_t smem, bool dependent,
+cudaError_t launch_clusters(void (*kernel)(A...), dim3 grid, int cluster, int threads, size_t smem, bool dependent,
                             cudaStream_t s, A... args) {
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1139,7 +1231,7 @@ cudaError_t launch_clusters(void (*kernel)(A...), unsigned grid, int cluster, in
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
@@ -1180,27 +1272,27 @@ cudaError_t launch_rows(const AdapterArgs& p, const DeviceInfo& dev, cudaStream_
         adapters_rows_kernel<W, true><<<(unsigned)grid, THREADS, 0, s>>>(p, (int)chunks, (int)iters);
         return cudaGetLastError();
     }
-    cudaError_t e = launch_group(p, ROWS, s);
+    cudaError_t e = p.scan ? cudaSuccess : launch_group(p, ROWS, s);
     if (e != cudaSuccess) return e;
-    return launch_clusters(adapters_rows_kernel<W, false>, (unsigned)grid, CL, THREADS, 0, true, s, p, (int)chunks, (int)iters);
+    return launch_clusters(adapters_rows_kernel<W, false>, (unsigned)grid, CL, THREADS, 0, !p.scan, s, p, (int)chunks, (int)iters);
 }
 
 template <class W, int CLT>
-cudaError_t launch_tiles(const AdapterArgs& p, cudaStream_t s) {
+cudaError_t launch_tiles(const AdapterArgs& p, int shares, cudaStream_t s) {
     const TileSmem lay(p.r, sizeof(W) == 4);
     const size_t smem = lay.total + 1024;
     int per_sm = 0;  // (raises the kernel's shared-memory limit)
     cudaError_t e = kernel_occupancy(reinterpret_cast<const void*>(adapters_tile_kernel<W, CLT>), TT, smem, &per_sm);
     if (e != cudaSuccess) return e;
-    e = launch_group(p, TM, s);
+    e = p.scan ? cudaSuccess : launch_group(p, TM, s);
     if (e != cudaSuccess) return e;
     const int64_t tiles = p.T / TM + std::min<int64_t>(p.n + 1, p.T);
-    return launch_clusters(adapters_tile_kernel<W, CLT>, (unsigned)(tiles * CLT), CLT, TT, smem, true, s, p);
+    return launch_clusters(adapters_tile_kernel<W, CLT>, dim3((unsigned)(tiles * CLT), (unsigned)shares), CLT, TT, smem, !p.scan, s, p);
 }
 
 // The choice of kernel and of the tile kernel's cluster, by what the steps of
 // either were measured to take (us; H = 256 .. 2048, N = 300 .. 16384):
-//   rows: 9 + 0.08 a tile of 8 rows + 0.9e-6 r (H + N) a tile;
+//   rows: 9 (grouped inside: 5) + 0.04 + 2.3e-5 N + 0.9e-6 r (H + N) a tile of 8;
 //   tiles: 4 + waves * (4 + 0.05 r + 0.6 a panel of H + 2 a block of y, per CTA),
 //   one CTA an SM (about 12 of 13 SMs can hold clusters of 4, and 15 clusters of
 //   8 fit).
@@ -1209,33 +1301,44 @@ cudaError_t launch_tiles(const AdapterArgs& p, cudaStream_t s) {
 // 22.3.)  A cluster must be wide enough that an accumulator of step 1 sums no
 // more than CHAIN panels: each addition truncates, and 4 CHAIN of them drift by
 // about 1e-6 of the sum.
+// CTAs that find their tiles by themselves save the grouping kernel and the start
+// of a second one, but do that work once a wave, 2 to 3 us each time: so the rows
+// kernel does while all its clusters can be resident at once, the tile kernel for
+// up to two waves (a grouping kernel before it -> by itself: 257 rows 12.4 -> 10.9
+// us, 947 rows 22.6 -> 20.7, 2048 rows in two waves 31.2 -> 29.1; in more waves
+// 512 rows of 64 adapters 19.6 -> 22.2, 2048 rows of 200 adapters 59 -> 97).
 template <class W>
-cudaError_t launch_typed(const AdapterArgs& p, const DeviceInfo& dev, cudaStream_t s) {
+cudaError_t launch_typed(AdapterArgs p, const DeviceInfo& dev, cudaStream_t s) {
     constexpr int CHAIN = 10;
-    if (p.T <= INLINE_T) return launch_rows<W>(p, dev, s);
+    const bool scans = p.T <= SCAN_T && p.n <= SCAN_N;
     const int n16 = (p.r + 15) / 16 * 16, accs = std::min(MAX_ACCS, (int)COLS_TMEM / n16 - 1), chunks = p.H / PK;
     // tiles of `rows` rows: one an adapter while adapters see fewer, else half a tile too many each
     const auto tiles = [&](int rows) {
         return (double)(p.T < (int64_t)rows * (p.n + 1) ? std::min<int64_t>(p.T, p.n + 1) : p.T / rows + (p.n + 1) / 2);
     };
     const double small = std::min<double>((double)p.T, (double)(p.T / ROWS + (p.n + 1) / 2));
-    double best = 9.0 + small * (0.08 + 0.9e-6 * p.r * (double)(p.H + p.N));
-    int cl = 0;
+    double best = (p.T <= INLINE_T ? 5.0 : 9.0) + small * (0.04 + 0.9e-6 * p.r * (double)(p.H + p.N) + 2.3e-5 * (double)p.N);
+    int cl = 0, shares = 1;
+    p.scan = scans && small * CL <= 3.0 * dev.sm_count;
     for (int c = 1; c <= CL; c *= 2) {
         if (chunks > c * accs * CHAIN) continue;
         const int slots = c <= 2 ? dev.sm_count : c == 4 ? dev.sm_count * 12 / 13 : 15 * CL * dev.sm_count / 148;
-        const double t = 4.0 + std::ceil(tiles(TM) * c / slots) *
-                                   (4.0 + 0.05 * p.r + 0.6 * chunks / c + 2.0 * (double)ceil_div(ceil_div(p.N, TM), c));
+        const int64_t blocks = ceil_div(p.N, (int64_t)TM * c);
+        const int q = (int)std::max(1.0, std::min({(double)blocks, std::floor(slots / (tiles(TM) * c)), 65535.0}));
+        const double waves = std::ceil(tiles(TM) * c * q / slots);
+        const double t = 4.0 + waves * (4.0 + 0.05 * p.r + 0.6 * chunks / c + 2.0 * (double)ceil_div(blocks, q));
         if (t < best) {
             best = t;
             cl = c;
+            shares = q;
+            p.scan = scans && waves <= 2.0;
         }
     }
     switch (cl) {
-        case 1: return launch_tiles<W, 1>(p, s);
-        case 2: return launch_tiles<W, 2>(p, s);
-        case 4: return launch_tiles<W, 4>(p, s);
-        case 8: return launch_tiles<W, 8>(p, s);
+        case 1: return launch_tiles<W, 1>(p, shares, s);
+        case 2: return launch_tiles<W, 2>(p, shares, s);
+        case 4: return launch_tiles<W, 4>(p, shares, s);
+        case 8: return launch_tiles<W, 8>(p, shares, s);
         default: return launch_rows<W>(p, dev, s);
     }
 }

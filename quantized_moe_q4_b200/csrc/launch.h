@@ -148,7 +148,9 @@ struct AdapterArgs {
     float* y;
     int64_t ldx, ldb, ldy, N, T;
     int H, r, n;
-    int wide;            // byte offsets in base or y pass 32 bits (set by launch_adapters)
+    // set by launch_adapters: byte offsets in base or y pass 32 bits; every CTA
+    // finds its tile by itself
+    int wide, scan;
     // workspace
     uint32_t* status;
     int32_t* n_tiles;
