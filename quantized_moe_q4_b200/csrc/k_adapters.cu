@@ -246,7 +246,8 @@ __device__ __forceinline__ void expand_columns(const W* b, const AdapterArgs& p,
         for (int k0 = 0; k0 < p.r; k0 += 8 * KF) {
             Raw8<W> raw[KF];
 #pragma unroll
-            for (int j = 0; j < KF; ++j) raw[j].load(row + min(k0 + 8 * j, p.r - 8));
+            for (int j = 0; j < KF; ++j)
+                if (k0 + 8 * j < p.r) raw[j].load(row + k0 + 8 * j);  // (uniform)
 #pragma unroll
             for (int j = 0; j < KF; ++j) {
                 const int k = k0 + 8 * j;
