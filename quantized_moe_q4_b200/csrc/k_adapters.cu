@@ -9,11 +9,21 @@
 // y, and r (H + N) elements of its adapter, so every kernel here is bound by
 // memory or latency; what matters is that the rank-r middle vector u = A x
 // never leaves the chip and that nothing is launched twice.
-//   - rows are grouped by adapter into tiles: inside the kernel up to
-//     INLINE_T rows (one launch), else by the grouping kernels (device only;
-//     the host never reads the counts);
-//   - a tile is the work of a cluster of 8 CTAs: they share A x through
-//     distributed shared memory, then each takes its own columns of y.
+//   - rows are grouped by adapter into tiles, on the device; the host never
+//     reads the counts.  Every CTA finds its tile by itself while that is
+//     cheaper than grouping kernels before it (one launch then);
+//   - a tile is the work of a cluster of CTAs, several clusters if there are
+//     many columns: they share u through distributed shared memory, then each
+//     takes its own columns of y;
+//   - tiles of 8 rows are computed with FMAs (rows kernel), tiles of 128 rows
+//     on the tensor cores (tile kernel); launch_typed says when.
+//
+// Device times, one B200 (hidden size 2048; calls one after another):
+//   rows kernel   1 row, 2048 outputs, rank 16                 4.1 us
+//                 64 rows of 64 adapters, the same              6.3 us
+//                 8 rows of 8 adapters, 131072 outputs         13.2 us
+//   tile kernel   947 rows in 4 runs, 2048 outputs, rank 64    21 us
+//                 16384 rows of 8 adapters, the same           107 us, 3.7 TB/s
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -416,8 +426,8 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(THREADS, 4)
 //      (SWIZZLE_128B).  The tensor core truncates each sum, so a long chain of
 //      additions drifts: the panels take turns on several accumulators, the lo
 //      products have one of their own, and all are added in binary32.  (Error
-//      of y - base at H = 2048, r = 64, CLT = 1: 8.4e-7 of its norm; a plain
-//      binary32 product has 8.3e-7.)
+//      of y - base at H = 2048, r = 64, bfloat16 weights: 7.2e-7 of its norm
+//      with CLT = 1 and 3.6e-7 with 8; a plain binary32 product has 8.2e-7.)
 //   2. the partial sums are joined through distributed shared memory: each CTA
 //      adds its share of the rows in rank order and hands them to all.
 //   3. d^T = B u^T over the CTA's blocks of 128 columns of y: M = columns of y,
@@ -428,9 +438,17 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(THREADS, 4)
 // for TMEM on other SMs cannot block each other in a ring.
 //
 // A kernel that uses TMEM gets one CTA an SM here, so the CTA is wide and its
-// parts run apart: 16 warps convert x, join u and later read base and write y;
-// 3 warps bring the panels of A and, without waiting for u, of B, a panel a
-// warp; one issues the MMAs.  They meet on mbarriers only.
+// parts run apart: 16 warps in two groups convert the panels of x and A in
+// turn, join u and later read base and write y; 3 warps (binary32: 2) bring the
+// panels of B without waiting for u, a panel a warp; one issues the MMAs.  They
+// meet on mbarriers only.
+//
+// What bounds it: a panel of step 1 takes 0.6 us, near the shared memory's
+// bandwidth (loads 256, stores 320 and the MMAs' reads 384 clocks); a block of
+// step 3 takes 2 to 2.5 us, base and y through DRAM.  With many tiles the two
+// alternate on an SM instead of overlapping: 16384 rows (386 MB through DRAM)
+// at 46% of the DRAM's rate, tensor pipe 19% active.  With few, the two cluster
+// barriers and the join add 4 to 5 us.
 
 constexpr int TM = 128;                 // rows of a tile; columns of y in a block
 constexpr int PK = 32;                  // columns of a panel (128 bytes of binary32)
@@ -1322,7 +1340,7 @@ cudaError_t launch_typed(AdapterArgs p, const DeviceInfo& dev, cudaStream_t s) {
     int cl = 0, shares = 1;
     p.scan = scans && small * CL <= 3.0 * dev.sm_count;
     for (int c = 1; c <= CL; c *= 2) {
-        if (chunks > c * accs * CHAIN) continue;
+        if (chunks > c * accs * CHAIN || (p.T <= INLINE_T && !scans)) continue;  // (few rows have no workspace to be grouped in)
         const int slots = c <= 2 ? dev.sm_count : c == 4 ? dev.sm_count * 12 / 13 : 15 * CL * dev.sm_count / 148;
         const int64_t blocks = ceil_div(p.N, (int64_t)TM * c);
         const int q = (int)std::max(1.0, std::min({(double)blocks, std::floor(slots / (tiles(TM) * c)), 65535.0}));
@@ -1332,7 +1350,7 @@ cudaError_t launch_typed(AdapterArgs p, const DeviceInfo& dev, cudaStream_t s) {
             best = t;
             cl = c;
             shares = q;
-            p.scan = scans && waves <= 2.0;
+            p.scan = scans && (waves <= 2.0 || p.T <= INLINE_T);
         }
     }
     switch (cl) {

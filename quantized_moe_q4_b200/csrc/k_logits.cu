@@ -20,6 +20,12 @@
 // memory.  Bound by the logits' bytes (read, and written if asked for) without
 // rules; with them a CTA spends half its time in the chain of dependent loads
 // (row, tokens, their logits), which two CTAs an SM cover in part.
+//
+// Device times, one B200, 131072 tokens:
+//   1 row with a history of 1000: 9.3 us (latency); 64 rows, histories of 2000,
+//   64 biases, masks: 34 us; 32 rows, histories of 16384: 23 us; 256 rows,
+//   histories of 1000, masks: 105 us, 2.6 TB/s; 256 rows copied without rules:
+//   41 to 43 us, 6.3 TB/s.
 #include <algorithm>
 #include <type_traits>
 

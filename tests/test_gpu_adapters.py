@@ -213,3 +213,39 @@ def test_no_rows():
 def test_the_lm_head_shape():
     A, x, e, base = make(17, 8, 2048, 131072, 16, 8, "fp16", list(range(8)))
     check(A, x, e, base, m.moe_q4_adapters_apply(A, x, e, base=base))
+
+
+@pytest.mark.parametrize("T,H,N,r,n,ids", [
+    (257, 256, 300, 8, 1, "none"),         # no row has an adapter
+    (300, 256, 300, 8, 255, "mixed"),      # the most adapters that a CTA finds its tile among
+    (2048, 256, 300, 16, 255, "runs"),
+    (2048, 256, 260, 64, 2, "mixed"),      # the most rows
+    (1025, 512, 513, 24, 3, "one"),
+    (640, 256, 40001, 16, 4, "runs"),      # several clusters a tile, a ragged last block
+    (300, 256, 70000, 64, 2, "mixed"),
+    (4000, 256, 9000, 32, 3, "runs"),
+    (200, 256, 20000, 64, 1, "one"),       # tensor cores for a batch below the grouping kernels' sizes
+    (250, 512, 30001, 128, 2, "runs"),
+])
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+def test_tiles_found_by_their_own_ctas(kind, T, H, N, r, n, ids):
+    A, x, e, base = make(T + N, T, H, N, r, n, kind, ids, pad=4)
+    y = m.moe_q4_adapters_apply(A, x, e, base=base)
+    check(A, x, e, base, y)
+    z = base.clone()  # in place
+    m.moe_q4_adapters_apply(A, x, e, base=z, y=z)
+    assert torch.equal(z, y)
+    check(A, x, e, None, m.moe_q4_adapters_apply(A, x, e))
+
+
+@pytest.mark.parametrize("T,H,N,r,n", [
+    (1, 256, 300, 8, 1), (128, 256, 4096, 128, 256), (256, 256, 4096, 128, 300), (256, 256, 20000, 64, 1),
+    (257, 256, 300, 8, 300), (512, 256, 4096, 64, 64), (2048, 256, 300, 16, 256), (2049, 256, 300, 16, 1), (20000, 256, 260, 16, 5),
+])
+def test_nothing_past_the_workspace_is_written(T, H, N, r, n):
+    A, x, e, base = make(T + n, T, H, N, r, n, "bf16")
+    need = m.moe_q4_adapters_workspace_bytes(A, T)
+    room = torch.full((need + (1 << 20),), 0x5A, dtype=torch.uint8, device="cuda")
+    y = m.moe_q4_adapters_apply(A, x, e, base=base, workspace=room[:need])
+    assert bool((room[need:] == 0x5A).all())
+    check(A, x, e, base, y)
