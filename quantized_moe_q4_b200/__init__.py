@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import numpy as np
@@ -89,13 +90,9 @@ class _Adapters(ctypes.Structure):
                 ("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
 
 
-class _LogitRules(ctypes.Structure):
-    _fields_ = [("vocab", ctypes.c_int64), ("tokens", ctypes.c_void_p), ("n_tokens", ctypes.c_int64),
-                ("row_start", ctypes.c_void_p), ("generated_start", ctypes.c_void_p),
-                ("repetition", ctypes.c_void_p), ("presence", ctypes.c_void_p), ("frequency", ctypes.c_void_p),
-                ("bias_token", ctypes.c_void_p), ("bias_value", ctypes.c_void_p), ("n_bias", ctypes.c_int64),
-                ("bias_start", ctypes.c_void_p), ("mask", ctypes.c_void_p), ("n_masks", ctypes.c_int64),
-                ("mask_row", ctypes.c_void_p)]
+# moe_q4_logit_rules: fifteen fields of 8 bytes (a step makes one, and packing is
+# quicker than a ctypes structure)
+_pack_rules = struct.Struct("15q").pack
 
 
 def _load() -> ctypes.CDLL:
@@ -413,14 +410,15 @@ def _vector(t, name: str, device: int, dtype, n=None):
         return None
     if t.dtype is not dtype or t.get_device() != device or t.dim() != 1 or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous 1D {dtype} tensor on GPU {device}")
-    if n is not None and t.shape[0] != n:
-        raise ValueError(f"{name} has {t.shape[0]} elements, expected {n}")
+    if n is not None and t.numel() != n:
+        raise ValueError(f"{name} has {t.numel()} elements, expected {n}")
     return t.data_ptr()
 
 
 def _call(f, what: str, device: int, stream, *args):
-    """f(*args, stream) with `device` current; stream None: its current one."""
-    if torch.cuda.current_device() != device:
+    """f(*args, stream) with `device` current; stream None: its current one.
+    (A tensor on it has initialised CUDA.)"""
+    if torch._C._cuda_getDevice() != device:
         with torch.cuda.device(device):
             return _call(f, what, device, stream, *args)
     rc = f(*args, torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream)
@@ -498,28 +496,43 @@ class LogitRules:
             raise ValueError("tokens and row_start belong together")
         if not (bias_token is None) == (bias_value is None) == (bias_start is None):
             raise ValueError("bias_token, bias_value and bias_start belong together")
-        self.tensors = dict(tokens=tokens, row_start=row_start, generated_start=generated_start,
-                            repetition=repetition, presence=presence, frequency=frequency, bias_token=bias_token,
-                            bias_value=bias_value, bias_start=bias_start, mask=mask, mask_row=mask_row)
+        self.tokens, self.row_start, self.generated_start = tokens, row_start, generated_start
+        self.repetition, self.presence, self.frequency = repetition, presence, frequency
+        self.bias_token, self.bias_value, self.bias_start = bias_token, bias_value, bias_start
+        self.mask, self.mask_row = mask, mask_row
 
-    def struct(self, T: int, V: int, device: int) -> _LogitRules:
+    def struct(self, T: int, V: int, device: int) -> bytes:
         """The C descriptor for T rows of V logits on a GPU."""
-        t = self.tensors
         i32, i64, f32 = torch.int32, torch.int64, torch.float32
-
-        def ptr(name, dtype, n=None):
-            return _vector(t[name], name, device, dtype, n)
-        mask = t["mask"]
-        if mask is not None and (mask.dtype is not i32 or mask.dim() != 2 or mask.shape[1] != (V + 31) // 32 or
-                                 mask.get_device() != device or not mask.is_contiguous()):
-            raise ValueError(f"mask must be a contiguous [n_masks, {(V + 31) // 32}] int32 tensor on GPU {device}")
-        n_bias = 0 if t["bias_token"] is None else t["bias_token"].shape[0]
-        return _LogitRules(
-            V, ptr("tokens", i32), 0 if t["tokens"] is None else t["tokens"].shape[0], ptr("row_start", i64, T + 1),
-            ptr("generated_start", i64, T), ptr("repetition", f32, T), ptr("presence", f32, T),
-            ptr("frequency", f32, T), ptr("bias_token", i32), ptr("bias_value", f32, n_bias), n_bias,
-            ptr("bias_start", i64, T + 1), None if mask is None else mask.data_ptr(),
-            0 if mask is None else mask.shape[0], ptr("mask_row", i32, T))
+        tokens = row_start = generated = rep = pres = freq = n_tokens = 0
+        bias_token = bias_value = bias_start = n_bias = masks = mask_row = n_masks = 0
+        if self.tokens is not None:
+            tokens = _vector(self.tokens, "tokens", device, i32)
+            n_tokens = self.tokens.shape[0]
+            row_start = _vector(self.row_start, "row_start", device, i64, T + 1)
+        if self.generated_start is not None:
+            generated = _vector(self.generated_start, "generated_start", device, i64, T)
+        if self.repetition is not None:
+            rep = _vector(self.repetition, "repetition", device, f32, T)
+        if self.presence is not None:
+            pres = _vector(self.presence, "presence", device, f32, T)
+        if self.frequency is not None:
+            freq = _vector(self.frequency, "frequency", device, f32, T)
+        if self.bias_token is not None:
+            bias_token = _vector(self.bias_token, "bias_token", device, i32)
+            n_bias = self.bias_token.shape[0]
+            bias_value = _vector(self.bias_value, "bias_value", device, f32, n_bias)
+            bias_start = _vector(self.bias_start, "bias_start", device, i64, T + 1)
+        mask = self.mask
+        if mask is not None:
+            if (mask.dtype is not i32 or mask.dim() != 2 or mask.shape[1] != (V + 31) // 32 or
+                    mask.get_device() != device or not mask.is_contiguous()):
+                raise ValueError(f"mask must be a contiguous [n_masks, {(V + 31) // 32}] int32 tensor on GPU {device}")
+            masks, n_masks = mask.data_ptr(), mask.shape[0]
+        if self.mask_row is not None:
+            mask_row = _vector(self.mask_row, "mask_row", device, i32, T)
+        return _pack_rules(V, tokens, n_tokens, row_start, generated, rep, pres, freq, bias_token, bias_value, n_bias,
+                           bias_start, masks, n_masks, mask_row)
 
 
 def moe_q4_logits_apply(rules: LogitRules, logits: torch.Tensor, out=None, token=None, lse=None, status=None,
@@ -536,7 +549,7 @@ def moe_q4_logits_apply(rules: LogitRules, logits: torch.Tensor, out=None, token
     if out is None and token is None and lse is None:
         out = torch.empty((T, V), dtype=torch.float32, device=logits.device)
     pout, ldo = (None, 0) if out is None else (out.data_ptr(), _rows(out, "out", dev, T, V))
-    _call(_lib.moe_q4_logits_apply, "moe_q4_logits_apply", dev, stream, ctypes.byref(rules.struct(T, V, dev)),
+    _call(_lib.moe_q4_logits_apply, "moe_q4_logits_apply", dev, stream, rules.struct(T, V, dev),
           logits.data_ptr(), ld, T, pout, ldo, _vector(token, "token", dev, torch.int32, T),
           _vector(lse, "lse", dev, torch.float32, T), _vector(status, "status", dev, torch.int32, 1))
     return out, token, lse
