@@ -510,12 +510,22 @@ __device__ __forceinline__ void arrive(uint64_t* bar) {
 }
 __device__ __forceinline__ void sync_rows() { asm volatile("bar.sync 1, %0;" ::"n"(ROW_THREADS) : "memory"); }
 
-// The tf32 value nearest to v (ties away from zero), as binary32.
-__device__ __forceinline__ float tf32_near(float v) { return __uint_as_float((__float_as_uint(v) + 0x1000u) & 0xffffe000u); }
+// The finite tf32 value nearest to v (ties away from zero), as binary32.  (Its
+// magnitude is at most the largest tf32 value, (2 - 2^-10) 2^127: a binary32
+// value above the middle between that and 2^128 would become infinite, its lo
+// part too, and their products NaN.)
+__device__ __forceinline__ float tf32_near(float v) {
+    float h;
+    asm("min.xorsign.abs.f32 %0, %1, %2;"
+        : "=f"(h)
+        : "f"(__uint_as_float((__float_as_uint(v) + 0x1000u) & 0xffffe000u)), "f"(__uint_as_float(0x7f7fe000u)));
+    return h;
+}
 
 // Four values as two tf32 parts, into the same place of two panels.  The lo
-// part (exact as a binary32 value, at most 2^-11 of v) is not rounded: the
-// MMA drops its low 13 bits, at most 2^-21 of v.
+// part (exact as a binary32 value, at most 2^-11 of v, 2^-10 beside the largest
+// tf32 value) is not rounded: the MMA drops its low 13 bits, at most 2^-21 of v,
+// or 2^-136 where it is subnormal.
 __device__ __forceinline__ void store_split(char* hi, char* lo, uint32_t at, float4 v) {
     const float4 h = make_float4(tf32_near(v.x), tf32_near(v.y), tf32_near(v.z), tf32_near(v.w));
     *reinterpret_cast<float4*>(hi + at) = h;
