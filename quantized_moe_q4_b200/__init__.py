@@ -5,6 +5,11 @@ kernels (sm_100a).  PyTorch provides device memory and streams.  The function
 names are the C ABI's (include/moe_q4.h).  Importing this module fails loudly
 if the CUDA library has not been built; there is no fallback.
 
+A call runs on `stream`, or on the current stream.  What it allocates (outputs
+and workspaces that are not given) belongs to that stream; an output it returns
+is marked as used by the current stream too.  Tensors that are given have to
+live, and to be ordered, as with any other work on a stream.
+
 The layer is the MoE expert FFN of "A 35B Hybrid-Attention Mixture-of-Experts
 Model on a 6GB 2011 GPU: Hand-Written 4-bit CUDA Inference for Fermi" (Dutch
 technical summary, Methodologie 1 and 2): top-k routing, Q8_0 activations,
@@ -159,6 +164,26 @@ def _check(rc: int, what: str):
         raise MoeQ4Error(rc, what)
 
 
+def _scratch(stream, make, *args, **kw) -> torch.Tensor:
+    """make(*args, **kw) on the stream of the call.  (A block of the caching
+    allocator that is freed is handed out again in the order of the stream that
+    it was allocated on: one of the current stream, freed on return, could be
+    somebody else's before the call's kernels on `stream` have run.)"""
+    if stream is None:
+        return make(*args, **kw)
+    with torch.cuda.stream(stream):
+        return make(*args, **kw)
+
+
+def _result(stream, make, *args, **kw) -> torch.Tensor:
+    """The same for what the call returns: the caller may use it, and let go of
+    it, on the current stream."""
+    t = _scratch(stream, make, *args, **kw)
+    if stream is not None:
+        t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
 def moe_q4_status_string(code: int) -> str:
     return _lib.moe_q4_status_string(int(code)).decode()
 
@@ -219,8 +244,8 @@ class Layer:
 
 def moe_q4_quantize_act(x: torch.Tensor, q=None, d=None, status=None, stream=None):
     T, H = x.shape
-    q = torch.empty((T, H), dtype=torch.int8, device=x.device) if q is None else q
-    d = torch.empty((T, H // QK), dtype=torch.int16, device=x.device) if d is None else d
+    q = _result(stream, torch.empty, (T, H), dtype=torch.int8, device=x.device) if q is None else q
+    d = _result(stream, torch.empty, (T, H // QK), dtype=torch.int16, device=x.device) if d is None else d
     _check(_lib.moe_q4_quantize_act(_p(x), T, H, _p(q), _p(d), _p(status), _stream(stream)), "moe_q4_quantize_act")
     return q, d
 
@@ -228,9 +253,9 @@ def moe_q4_quantize_act(x: torch.Tensor, q=None, d=None, status=None, stream=Non
 def moe_q4_route(layer: Layer, x: torch.Tensor, topk_idx=None, topk_w=None, logits=None, stream=None):
     T = x.shape[0]
     k, E = layer.top_k, layer.n_experts
-    topk_idx = torch.empty((T, k), dtype=torch.int32, device=x.device) if topk_idx is None else topk_idx
-    topk_w = torch.empty((T, k), dtype=torch.float32, device=x.device) if topk_w is None else topk_w
-    logits = torch.empty((T, E), dtype=torch.float32, device=x.device) if logits is None else logits
+    topk_idx = _result(stream, torch.empty, (T, k), dtype=torch.int32, device=x.device) if topk_idx is None else topk_idx
+    topk_w = _result(stream, torch.empty, (T, k), dtype=torch.float32, device=x.device) if topk_w is None else topk_w
+    logits = _result(stream, torch.empty, (T, E), dtype=torch.float32, device=x.device) if logits is None else logits
     _check(_lib.moe_q4_route(layer.ref, _p(x), T, _p(topk_idx), _p(topk_w), _p(logits), _stream(stream)),
            "moe_q4_route")
     return topk_idx, topk_w, logits
@@ -253,9 +278,9 @@ def alloc_workspace(nbytes: int, device="cuda") -> torch.Tensor:
 
 def moe_q4_ffn_forward(layer: Layer, x: torch.Tensor, y=None, workspace=None, stream=None):
     T = x.shape[0]
-    y = torch.empty_like(x) if y is None else y
+    y = _result(stream, torch.empty_like, x) if y is None else y
     if workspace is None:
-        workspace = alloc_workspace(moe_q4_ffn_workspace_bytes(layer, T), x.device)
+        workspace = _scratch(stream, alloc_workspace, moe_q4_ffn_workspace_bytes(layer, T), x.device)
     _check(_lib.moe_q4_ffn_forward(layer.ref, _p(x), T, _p(y), _p(workspace), workspace.numel(),
                                    _stream(stream)), "moe_q4_ffn_forward")
     return y
@@ -319,7 +344,7 @@ def workspace_views(layer: Layer, T: int, ws: torch.Tensor) -> dict:
 
 def moe_q4_block_dots(w_blocks: torch.Tensor, qa: torch.Tensor, out=None, stream=None):
     n = w_blocks.numel() // Q4_BYTES
-    out = torch.empty(n, dtype=torch.int32, device=w_blocks.device) if out is None else out
+    out = _result(stream, torch.empty, n, dtype=torch.int32, device=w_blocks.device) if out is None else out
     _check(_lib.moe_q4_block_dots(_p(w_blocks), _p(qa), n, _p(out), _stream(stream)), "moe_q4_block_dots")
     return out
 
@@ -339,7 +364,7 @@ def moe_q4_ffn_forward_noalloc(layer: Layer, x: torch.Tensor, y=None, stream=Non
     caller workspace (for callers that cannot allocate device memory; see
     include/moe_q4.h).  Calls that overlap on the GPU race on the scratch."""
     T = x.shape[0]
-    y = torch.empty_like(x) if y is None else y
+    y = _result(stream, torch.empty_like, x) if y is None else y
     _check(_lib.moe_q4_ffn_forward_noalloc(layer.ref, _p(x), T, _p(y), _stream(stream)),
            "moe_q4_ffn_forward_noalloc")
     return y
@@ -351,7 +376,7 @@ def moe_q4_residual_rmsnorm(x: torch.Tensor, y=None, eps: float = 1e-6, xn=None,
     """x <- x + y (if y is given, in place), then returns xn = RMSNorm(x) (unit
     gain over the last dimension), written into `xn` if given."""
     T, H = x.shape
-    xn = torch.empty_like(x) if xn is None else xn
+    xn = _result(stream, torch.empty_like, x) if xn is None else xn
     _check(_lib.moe_q4_residual_rmsnorm(_p(x), _p(y), T, H, float(eps), _p(xn), _stream(stream)),
            "moe_q4_residual_rmsnorm")
     return xn
@@ -366,7 +391,7 @@ def moe_q4_stack_forward(layers, x: torch.Tensor, eps: float = 1e-6, workspace=N
     T = x.shape[0]
     arr = (_Layer * len(layers))(*[l.struct for l in layers])
     if workspace is None:
-        workspace = alloc_workspace(moe_q4_stack_workspace_bytes(layers[0], T), x.device)
+        workspace = _scratch(stream, alloc_workspace, moe_q4_stack_workspace_bytes(layers[0], T), x.device)
     _check(_lib.moe_q4_stack_forward(arr, len(layers), _p(x), T, float(eps), _p(workspace), workspace.numel(),
                                      _stream(stream)), "moe_q4_stack_forward")
     return x
@@ -383,9 +408,9 @@ def moe_q4_gemv(W: torch.Tensor, x: torch.Tensor, y=None, workspace=None, stream
     the Q8_0 form of x [T, H] (T <= 8)."""
     T, H = x.shape
     N = W.shape[0]
-    y = torch.empty((T, N), dtype=torch.float32, device=x.device) if y is None else y
+    y = _result(stream, torch.empty, (T, N), dtype=torch.float32, device=x.device) if y is None else y
     if workspace is None:
-        workspace = alloc_workspace(moe_q4_gemv_workspace_bytes(T, H), x.device)
+        workspace = _scratch(stream, alloc_workspace, moe_q4_gemv_workspace_bytes(T, H), x.device)
     _check(_lib.moe_q4_gemv(_p(W), N, H, _p(x), T, _p(y), _p(workspace), workspace.numel(), _stream(stream)),
            "moe_q4_gemv")
     return y
@@ -468,11 +493,11 @@ def moe_q4_adapters_apply(adapters: Adapters, x: torch.Tensor, adapter: torch.Te
     ldx = _rows(x, "x", dev, T, adapters.hidden)
     ids = _vector(adapter, "adapter", dev, torch.int32, T)
     if y is None:
-        y = torch.empty((T, N), dtype=torch.float32, device=x.device)
+        y = _result(stream, torch.empty, (T, N), dtype=torch.float32, device=x.device)
     ldy = _rows(y, "y", dev, T, N)
     pbase, ldb = (None, 0) if base is None else (base.data_ptr(), _rows(base, "base", dev, T, N))
     if workspace is None:
-        workspace = alloc_workspace(moe_q4_adapters_workspace_bytes(adapters, T), x.device)
+        workspace = _scratch(stream, alloc_workspace, moe_q4_adapters_workspace_bytes(adapters, T), x.device)
     elif workspace.get_device() != dev or workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous uint8 tensor on GPU {dev}")
     _call(_lib.moe_q4_adapters_apply, "moe_q4_adapters_apply", dev, stream, adapters.ref, x.data_ptr(), ldx, ids, T,
@@ -547,7 +572,7 @@ def moe_q4_logits_apply(rules: LogitRules, logits: torch.Tensor, out=None, token
     dev = logits.get_device()
     ld = _rows(logits, "logits", dev, T, V)
     if out is None and token is None and lse is None:
-        out = torch.empty((T, V), dtype=torch.float32, device=logits.device)
+        out = _result(stream, torch.empty, (T, V), dtype=torch.float32, device=logits.device)
     pout, ldo = (None, 0) if out is None else (out.data_ptr(), _rows(out, "out", dev, T, V))
     _call(_lib.moe_q4_logits_apply, "moe_q4_logits_apply", dev, stream, rules.struct(T, V, dev),
           logits.data_ptr(), ld, T, pout, ldo, _vector(token, "token", dev, torch.int32, T),
@@ -566,11 +591,11 @@ def moe_q4_ffn_forward_streamed(layer: Layer, x: torch.Tensor, y=None, workspace
     Layer.from_host_pinned): the experts the routing selects are copied into
     `staging` on the device, then the layer runs there."""
     T = x.shape[0]
-    y = torch.empty_like(x) if y is None else y
+    y = _result(stream, torch.empty_like, x) if y is None else y
     if workspace is None:
-        workspace = alloc_workspace(moe_q4_ffn_workspace_bytes(layer, T), x.device)
+        workspace = _scratch(stream, alloc_workspace, moe_q4_ffn_workspace_bytes(layer, T), x.device)
     if staging is None:
-        staging = alloc_workspace(moe_q4_staging_bytes(layer), x.device)
+        staging = _scratch(stream, alloc_workspace, moe_q4_staging_bytes(layer), x.device)
     _check(_lib.moe_q4_ffn_forward_streamed(layer.ref, _p(x), T, _p(y), _p(workspace), workspace.numel(),
                                             _p(staging), staging.numel(), _stream(stream)),
            "moe_q4_ffn_forward_streamed")
