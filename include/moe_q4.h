@@ -269,8 +269,9 @@ int moe_q4_gemv(const uint8_t* W, int64_t N, int32_t H, const float* x, int64_t 
  * moe_q4_ffn_forward, N = hidden).  The paper has no counterpart.
  *   - x [T] rows of hidden fp32 at a pitch of ldx elements (ldx >= hidden, a
  *     multiple of 4); base and y [T] rows of n_out fp32 at pitches ldb and
- *     ldy (>= n_out, any).  base NULL: zeros.  base == y with ldb == ldy:
- *     in place, rows without an adapter are then neither read nor written.
+ *     ldy (>= n_out, any).  base NULL: zeros, and ldb is not looked at.
+ *     base == y with ldb == ldy: in place, rows without an adapter are then
+ *     neither read nor written.
  *   - adapter [T] int32 on the device, in any order; an index outside
  *     [-1, n_adapters) counts as -1 and sets MOE_Q4_STATUS_BAD_ADAPTER_INDEX.
  *   - a and b are fp32, binary16 or bfloat16 (dtype).  x, A x and fp32

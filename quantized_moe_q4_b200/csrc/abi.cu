@@ -622,7 +622,7 @@ int moe_q4_adapters_apply(const moe_q4_adapters* A, const float* x, int64_t ldx,
     if (rc) return rc;
     p.a = A->a; p.b = A->b; p.scale = A->scale;
     p.x = x; p.ids = adapter; p.base = base; p.y = y;
-    p.ldx = ldx; p.ldb = ldb; p.ldy = ldy; p.N = N; p.T = T;
+    p.ldx = ldx; p.ldb = base ? ldb : 0; p.ldy = ldy; p.N = N; p.T = T;  // (without base, ldb may be anything)
     p.H = A->hidden; p.r = A->rank; p.n = A->n_adapters;
     return cuda_rc(launch_adapters(p, A->dtype, dev, reinterpret_cast<cudaStream_t>(stream)));
 }
