@@ -270,8 +270,8 @@ int moe_q4_gemv(const uint8_t* W, int64_t N, int32_t H, const float* x, int64_t 
  *   - x [T] rows of hidden fp32 at a pitch of ldx elements (ldx >= hidden, a
  *     multiple of 4); base and y [T] rows of n_out fp32 at pitches ldb and
  *     ldy (>= n_out, any).  base NULL: zeros, and ldb is not looked at.
- *     base == y with ldb == ldy: in place, rows without an adapter are then
- *     neither read nor written.
+ *     base == y with ldb == ldy (of a single row, any two): in place, rows
+ *     without an adapter are then neither read nor written.
  *   - adapter [T] int32 on the device, in any order; an index outside
  *     [-1, n_adapters) counts as -1 and sets MOE_Q4_STATUS_BAD_ADAPTER_INDEX.
  *   - a and b are fp32, binary16 or bfloat16 (dtype).  x, A x and fp32
@@ -341,7 +341,8 @@ int moe_q4_adapters_apply(const moe_q4_adapters* A, const float* x, int64_t ldx,
  *   - Start positions outside [0, n_tokens] or [0, n_bias] are clamped to it.
  * Outputs, each optional but at least one:
  *   out [T] rows of vocab fp32 at pitch ld_out: the processed logits
- *     (out == logits with the same pitch: in place; no other overlap).
+ *     (out == logits with the same pitch, of a single row with any: in
+ *     place; no other overlap).
  *   token [T] int32: the largest processed logit's token, the lowest one on
  *     ties; -1 where no logit is above -inf.  NaN ranks below every number.
  *   lse [T] fp32: log(sum_v exp(processed logit)), so that token's

@@ -615,7 +615,7 @@ int moe_q4_adapters_apply(const moe_q4_adapters* A, const float* x, int64_t ldx,
         overlap(y, ybytes, workspace, need) || overlap(y, ybytes, A->a, wbytes * (size_t)H) ||
         overlap(y, ybytes, A->b, wbytes * (size_t)N) ||
         (A->scale && overlap(y, ybytes, A->scale, sizeof(float) * (size_t)A->n_adapters)) ||
-        (base && !(base == y && ldb == ldy) && rows_overlap(base, ldb, N, y, ldy, N, T)))
+        (base && !(base == y && (ldb == ldy || T == 1)) && rows_overlap(base, ldb, N, y, ldy, N, T)))
         return MOE_Q4_ERR_OVERLAP;
     DeviceInfo dev;
     rc = current_device(&dev);
@@ -672,7 +672,7 @@ int moe_q4_logits_apply(const moe_q4_logit_rules* R, const float* logits, int64_
         if (i && overlap(outs[i].p, outs[i].n, logits, 4 * ((rows - 1) * (size_t)ld + (size_t)V)))
             return MOE_Q4_ERR_OVERLAP;
     }
-    if (out && !(out == logits && ld_out == ld) && rows_overlap(logits, ld, V, out, ld_out, V, T))
+    if (out && !(out == logits && (ld_out == ld || T == 1)) && rows_overlap(logits, ld, V, out, ld_out, V, T))
         return MOE_Q4_ERR_OVERLAP;
     DeviceInfo dev;
     int rc = current_device(&dev);
