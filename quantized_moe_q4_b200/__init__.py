@@ -554,6 +554,8 @@ class LogitRules:
                     mask.get_device() != device or not mask.is_contiguous()):
                 raise ValueError(f"mask must be a contiguous [n_masks, {(V + 31) // 32}] int32 tensor on GPU {device}")
             masks, n_masks = mask.data_ptr(), mask.shape[0]
+            if n_masks < 1 and T > 0:  # (an empty tensor has no address: it would count as no mask)
+                raise ValueError("mask has no rows")
         if self.mask_row is not None:
             mask_row = _vector(self.mask_row, "mask_row", device, i32, T)
         return _pack_rules(V, tokens, n_tokens, row_start, generated, rep, pres, freq, bias_token, bias_value, n_bias,
