@@ -903,6 +903,7 @@ __global__ void __launch_bounds__(TT, 1) adapters_tile_kernel(const __grid_const
     const int quad = warp & 3;      // the TMEM lanes that this warp reads are 32 quad .. + 31
     wait(&s_sums, 0);
     tc_fence_after_sync();
+    __syncwarp();  // (lanes may leave the wait apart; tcgen05.ld takes a converged warp)
     for (int c = warp >> 2; c < r / 8; c += ROW_WARPS / 4) {
         const uint32_t at = s_tmem + (uint32_t)((quad * 32) << 16) + 8u * c;
         float sum[8];
