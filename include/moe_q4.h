@@ -266,7 +266,9 @@ int moe_q4_gemv(const uint8_t* W, int64_t N, int32_t H, const float* x, int64_t 
  *     y[t] = base[t]                                  (a == -1: no adapter)
  * beside moe_q4_gemv (x its input, base its output, N the vocabulary) or
  * beside the expert layer (x and base the input and output of
- * moe_q4_ffn_forward, N = hidden).  The paper has no counterpart.
+ * moe_q4_ffn_forward, N = hidden; moe_q4_stack_forward runs its layers in one
+ * call, so this is for callers who run the layers themselves).  The paper has
+ * no counterpart.
  *   - x [T] rows of hidden fp32 at a pitch of ldx elements (ldx >= hidden, a
  *     multiple of 4); base and y [T] rows of n_out fp32 at pitches ldb and
  *     ldy (>= n_out, any).  base NULL: zeros, and ldb is not looked at.
@@ -276,8 +278,10 @@ int moe_q4_gemv(const uint8_t* W, int64_t N, int32_t H, const float* x, int64_t 
  *     [-1, n_adapters) counts as -1 and sets MOE_Q4_STATUS_BAD_ADAPTER_INDEX.
  *   - a and b are fp32, binary16 or bfloat16 (dtype).  x, A x and fp32
  *     adapters keep 21 significant bits or more in every product (all of
- *     them in small batches), and all sums are fp32.  A lower
- *     rank than `rank` is stored with zero rows of a / columns of b.
+ *     them in small batches; in large ones a value below 2^-115 is within
+ *     2^-136 of itself), and all sums are fp32.  All adapters have one rank: a
+ *     lower one than `rank` is stored with zero rows of a / columns of b, and
+ *     costs as much.
  *   - A row's result depends on that row and its adapter, on the shapes (T
  *     among them) through the choice of kernel, and on no other row; the same
  *     call gives the same bits.  x must be finite (a row that is not spoils
@@ -291,7 +295,9 @@ int moe_q4_gemv(const uint8_t* W, int64_t N, int32_t H, const float* x, int64_t 
  *     of one wider buffer (equal pitches).
  *   - The workspace (moe_q4_adapters_workspace_bytes(A, T) bytes, its first
  *     uint32 the status word, written by this call) may not be shared by
- *     calls that overlap on the GPU.  No host synchronisation; capturable.
+ *     calls that overlap on the GPU.  MOE_Q4_STATUS_SPIN_TIMEOUT in that
+ *     word: a wait inside the kernel gave up, and y is not to be used.  No
+ *     host synchronisation; capturable.
  * --------------------------------------------------------------------- */
 enum { MOE_Q4_F32 = 0, MOE_Q4_F16 = 1, MOE_Q4_BF16 = 2 };
 

@@ -6,9 +6,10 @@
 // the page has no counterpart of the per-request corrections.
 //
 // Work per row is 2 r (H + N) operations on 4 (H + 2 N) bytes of x, base and
-// y, and r (H + N) elements of its adapter, so every kernel here is bound by
-// memory or latency; what matters is that the rank-r middle vector u = A x
-// never leaves the chip and that nothing is launched twice.
+// y, and r (H + N) elements of its adapter: batches of up to about 1000 rows
+// are bound by latency, larger ones by DRAM and, where x passes through the
+// shared memory as two parts, by that.  What matters is that the rank-r middle
+// vector u = A x never leaves the chip and that nothing is launched twice.
 //   - rows are grouped by adapter into tiles, on the device; the host never
 //     reads the counts.  Every CTA finds its tile by itself while that is
 //     cheaper than grouping kernels before it (one launch then);
@@ -18,12 +19,14 @@
 //   - tiles of 8 rows are computed with FMAs (rows kernel), tiles of 128 rows
 //     on the tensor cores (tile kernel); launch_typed says when.
 //
-// Device times, one B200 (hidden size 2048; calls one after another):
-//   rows kernel   1 row, 2048 outputs, rank 16                 4.1 us
+// Device times, one B200 (hidden size 2048; calls one after another, inputs of
+// the smaller ones in L2; from DRAM those take 2 us more):
+//   rows kernel   1 row, 2048 outputs, rank 16                 4.0 us
 //                 64 rows of 64 adapters, the same              6.3 us
-//                 8 rows of 8 adapters, 131072 outputs         13.2 us
-//   tile kernel   947 rows in 4 runs, 2048 outputs, rank 64    21 us
-//                 16384 rows of 8 adapters, the same           107 us, 3.7 TB/s
+//                 8 rows of 8 adapters, 131072 outputs         13.5 us
+//   tile kernel   947 rows in runs of 4 adapters, 2048 outputs, rank 64, 16-bit
+//                 weights 21 us, binary32 25 us
+//                 16384 rows of 8 adapters, the same           108 and 136 us
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -689,7 +692,10 @@ __global__ void __launch_bounds__(TT, 1) adapters_tile_kernel(const __grid_const
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    // every wait is bounded; one that gives up is reported and not repeated
+    // Every wait on an mbarrier is bounded; one that gives up (after about 2 s)
+    // is reported and not repeated.  (The status word was stored when the rows
+    // were grouped, or by CTA (0, 0) as it started: long before, though nothing
+    // but the CTAs' usual order of starting puts that store first.)
     bool alive = true;
     const auto wait = [&](uint64_t* bar, uint32_t parity) {
         if (alive && !mbar_wait_bounded(bar, parity, 1u << 22)) {
@@ -1330,7 +1336,9 @@ cudaError_t launch_tiles(const AdapterArgs& p, int shares, cudaStream_t s) {
 // 1024 rows 25.9 and 19.8.  Rank 64: 256 rows 18.3 and 21.5; 512 rows 26.1 and
 // 22.3.)  A cluster must be wide enough that an accumulator of step 1 sums no
 // more than CHAIN panels: each addition truncates, and 4 CHAIN of them drift by
-// about 1e-6 of the sum.
+// about 1e-6 of the sum.  Where 8 CTAs are too few for that, the rows kernel is
+// left, at any T: above H = 7680 at ranks 104 to 128, 10240 at 88 and 96, 12800 at
+// 72 and 80 (2048 rows, 2048 outputs, rank 128: H = 7680 83 us, 7936 244 us).
 // CTAs that find their tiles by themselves save the grouping kernel and the start
 // of a second one, but do that work once a wave, 2 to 3 us each time: so the rows
 // kernel does while all its clusters can be resident at once, the tile kernel for

@@ -22,10 +22,15 @@
 // (row, tokens, their logits), which two CTAs an SM cover in part.
 //
 // Device times, one B200, 131072 tokens:
-//   1 row with a history of 1000: 9.3 us (latency); 64 rows, histories of 2000,
+//   1 row with a history of 1000: 9.2 us (latency); 64 rows, histories of 2000,
 //   64 biases, masks: 34 us; 32 rows, histories of 16384: 23 us; 256 rows,
-//   histories of 1000, masks: 105 us, 2.6 TB/s; 256 rows copied without rules:
-//   41 to 43 us, 6.3 TB/s.
+//   histories of 1000, masks: 105 us, 2.6 TB/s (token and log-sum-exp only:
+//   98 us); 256 rows without rules: all outputs 63 us, logits only 44 us, 6.1
+//   TB/s, token and log-sum-exp only 49 us.
+// Past 131072 tokens a CTA of eight holds more than STEP logits, so its stream
+// takes a second turn, and from about 141,000 on (with a mask) its tables leave
+// room for one CTA an SM only: the 64 rows above take 39 us at 131104 tokens, 69
+// at 151936 and 82 at 248320.
 #include <algorithm>
 #include <type_traits>
 
@@ -450,10 +455,11 @@ __global__ void __launch_bounds__(THREADS, 2) logits_kernel(const __grid_constan
 }  // namespace
 
 cudaError_t launch_logits(const LogitArgs& p, const DeviceInfo& dev, cudaStream_t s) {
-    // CTAs a row, two an SM at a time: a CTA takes about 6 us for the rules (3
+    // CTAs a row, two an SM at a time (counted so for large vocabularies too,
+    // where one fits): a CTA takes about 6 us for the rules (3
     // without) and 3 us for STEP logits, so as many as make the fewest turns,
     // each with at most STEP logits where 8 CTAs allow that.  (16 CTAs of 256
-    // threads a row: 8.2 us for one row of 131072 instead of 9.3, but 39 for 64
+    // threads a row: 8.2 us for one row of 131072 instead of 9.2, but 39 for 64
     // rows with histories instead of 34, and 30 for 32 rows of 16384 tokens each
     // instead of 23.)
     int ncl = 1;

@@ -4,9 +4,9 @@ its own.
 A bound for every element has to allow for roundings that all go the same way;
 at large ranks and hidden sizes it is so wide that one dropped part of a split
 value would pass.  Against the norm of the correction such a part is plain: a
-value kept to the 11 bits of one tf32 is off by up to 2^-12 of itself, 1.4e-4
-in the mean square, and independent errors of the terms leave that ratio as it
-is in their sums.
+value kept to the 11 bits of one tf32 is off by up to 2^-11 of itself, 2e-4 in
+the mean square, and independent errors of the terms leave that ratio as it is
+in their sums.
 
 What the kernels may lose, in units of u = 2^-24 of the norm, each at its
 largest: two-part values x, u and binary32 A and B 8 each (2^-21) and 4 for
