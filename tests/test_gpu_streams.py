@@ -103,3 +103,19 @@ def test_a_result_let_go_of_on_the_current_stream_is_not_overwritten_by_the_next
     assert z.data_ptr() != at
     torch.cuda.synchronize()
     assert torch.equal(kept, want) and torch.equal(z, want)
+
+
+@pytest.mark.parametrize("T", [8, 300, 1500, 9000])
+def test_calls_on_two_streams_at_once(T):
+    """Two adapter calls and logit rules in flight together, each with a workspace of its own."""
+    calls = [adapters(T), adapters(T + 1), logits()]
+    want = [c(None) for c in calls]
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    got = [[] for _ in calls]
+    for _ in range(10):
+        for c, s, g in zip(calls, streams, got):
+            g.append(c(s))
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        assert all(torch.equal(y, w) for y in g)
